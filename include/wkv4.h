@@ -295,6 +295,84 @@ WKV4_API size_t wkv4_forward_host_workspace(int64_t B, int64_t T, int64_t C, int
                                             int64_t chunk_steps);
 
 /*
+ * Backward pass of the forward (or, with r, of the gated forward): the
+ * gradients of a loss L with respect to every input of
+ *   out_t = s_t y_t,  y_t = (A_t + e^{u+k_t} v_t) / (D_t + e^{u+k_t}),
+ * s_t = sigmoid(r_t) (1 without r), A and D the state's sums as above, from
+ * gy = dL/dout and, when the state after the last step went on to be used,
+ * gstate_out = dL/d(state after the last step).  The forward is recomputed
+ * from k, v: nothing of it has to be kept but the inputs.
+ *   w, u        [C] fp32.
+ *   k, v        [B][T][C] in `dtype`; r likewise, or NULL: no gate.
+ *   state_in    [3][B][C] fp32, or NULL for the empty state.
+ *   gy          [B][T][C] in `dtype`.
+ *   state_out   [3][B][C] fp32, the forward's state after the last step;
+ *               required with gstate_out, else not read.
+ *   gstate_out  [3][B][C] fp32 or NULL (zero): the derivatives by the planes
+ *               num and den of state_out at the max it holds.  The max plane
+ *               of gstate_out is not read: the max only fixes the unit num
+ *               and den are held in (A = num e^max, D = den e^max), and what
+ *               depends on A and D alone has there num g_num + den g_den.
+ *   gk, gv      [B][T][C] in `dtype`, rounded once from fp32.
+ *   gr          [B][T][C] in `dtype`; required with r, else not written.
+ *   gw, gu      [C] fp32, summed over B and T in fp32 in a fixed order (the
+ *               same bits every time).
+ *   gstate_in   [3][B][C] fp32 or NULL; needs state_in.  All three planes:
+ *               e^max dL/dA, e^max dL/dD, and num g_num + den g_den.
+ *   workspace   device memory of at least wkv4_backward_workspace(B, T, C,
+ *               dtype) bytes, 16-byte aligned (may be NULL where that is 0),
+ *               for this call alone until the stream has passed it.
+ * No output may overlap an input, the workspace or another output:
+ * WKV4_ERR_ALIAS.  T == 0: gstate_in <- gstate_out's share (the state passes
+ * through), gw = gu = 0.  B == 0 or C == 0: nothing is written but gw and gu
+ * (zero).  A NULL required pointer, a workspace that is too small or
+ * misaligned, or T above 2^24 steps: WKV4_ERR_ARG.  Asynchronous on `stream`;
+ * no allocation.
+ */
+WKV4_API int wkv4_backward(int64_t B, int64_t T, int64_t C, const float* w, const float* u,
+                           const void* k, const void* v, const void* r, const float* state_in,
+                           const void* gy, const float* state_out, const float* gstate_out,
+                           void* gk, void* gv, void* gr, float* gw, float* gu, float* gstate_in,
+                           void* workspace, size_t workspace_bytes, wkv4_stream_t stream,
+                           int dtype);
+
+/* Workspace bytes wkv4_backward needs for these sizes (0 for B or C <= 0, T < 0
+ * or an unknown dtype). */
+WKV4_API size_t wkv4_backward_workspace(int64_t B, int64_t T, int64_t C, int dtype);
+
+/*
+ * Backward pass of wkv4_token_shift, from the gradients of its outputs:
+ *   gx[b,t]    = sum_i mix_i g_i[b,t] + sum_i (1 - mix_i) g_i[b,t+1]
+ *                (the second sum for t + 1 < T; plus gx_last[b] at t = T - 1),
+ *   gx_prev[b] = sum_i (1 - mix_i) g_i[b,0],
+ *   gmix_i     = sum_{b,t} g_i[b,t] (x[b,t] - x[b,t-1]),
+ * over the two or three outputs i = k, v(, r).
+ *   x, x_prev, mix_k, mix_v, mix_r   as given to wkv4_token_shift.
+ *   gxk, gxv, gxr  [B][T][C] in `dtype`: gradients of xk, xv, xr (gxr is
+ *                  required with mix_r and not read without).
+ *   gx_last        [B][C] in `dtype` or NULL (zero): gradient of x_last.
+ *   gx             [B][T][C] in `dtype`, rounded once from fp32.
+ *   gx_prev        [B][C] in `dtype` or NULL; may be asked for without x_prev
+ *                  (the gradient by a previous token that was zero).
+ *   gmix_k, gmix_v, gmix_r  [C] fp32, summed in fp32 in a fixed order.
+ *   workspace      device memory of at least wkv4_token_shift_backward_workspace
+ *                  (B, T, C, mix_r != NULL) bytes, 16-byte aligned.
+ * T == 0: gx_prev <- gx_last (or zero), the gmix zero.  Limits on B and T,
+ * overlaps and errors as wkv4_token_shift and wkv4_backward.
+ */
+WKV4_API int wkv4_token_shift_backward(int64_t B, int64_t T, int64_t C, const void* x,
+                                       const void* x_prev, const float* mix_k, const float* mix_v,
+                                       const float* mix_r, const void* gxk, const void* gxv,
+                                       const void* gxr, const void* gx_last, void* gx,
+                                       void* gx_prev, float* gmix_k, float* gmix_v, float* gmix_r,
+                                       void* workspace, size_t workspace_bytes,
+                                       wkv4_stream_t stream, int dtype);
+
+/* Workspace bytes wkv4_token_shift_backward needs (with_r: mix_r given); 0 for
+ * B, T or C <= 0. */
+WKV4_API size_t wkv4_token_shift_backward_workspace(int64_t B, int64_t T, int64_t C, int with_r);
+
+/*
  * Device-side error word of the current device (bit 1: a bounded wait for a
  * TMA copy ran out; bit 2: a bounded wait for a cluster peer's partial state
  * ran out; bit 8: a slot-indexed decode row named a slot outside its pool;

@@ -8,6 +8,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,8 +18,8 @@ LIB = os.path.join(PKG, "libwkv4.so")
 # the bounds-checked build (WKV4_CHECKED: every global index checked, fault
 # injection switches read from the environment), for the failure tests
 CHECKED_LIB = os.path.join(PKG, "libwkv4_checked.so")
-SOURCES = [os.path.join(CSRC, "wkv4_kernels.cu"), os.path.join(CSRC, "wkv4_api.cpp"),
-           os.path.join(CSRC, "wkv4_host.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("wkv4_kernels.cu", "wkv4_train.cu", "wkv4_api.cpp",
+                                           "wkv4_host.cpp")]
 
 
 def deps():
@@ -33,8 +34,8 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-    "-shared", "-cudart", "static",
 ]
+LINK_FLAGS = ["-shared", "-cudart", "static"]
 
 
 def nvcc() -> str:
@@ -68,10 +69,20 @@ def build(force: bool = False, verbose: bool = False, out: str = LIB, defines=()
     if out == LIB and not defines and not force and not stale():
         return LIB
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE, "-o", tmp, *SOURCES]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.check_call(cmd)
+    common = [nvcc(), *NVCC_FLAGS, *[f"-D{d}" for d in defines], "-I", INCLUDE]
+    with tempfile.TemporaryDirectory() as obj:  # the sources side by side, then one link
+        objects = [os.path.join(obj, os.path.basename(src) + ".o") for src in SOURCES]
+        jobs = []
+        for src, o in zip(SOURCES, objects):
+            cmd = [*common, "-c", "-o", o, src]
+            if verbose:
+                print(" ".join(cmd), flush=True)
+            jobs.append((cmd, subprocess.Popen(cmd)))
+        codes = [p.wait() for _, p in jobs]
+        for (cmd, _), code in zip(jobs, codes):
+            if code != 0:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.check_call([*common, *LINK_FLAGS, "-o", tmp, *objects])
     os.replace(tmp, out)
     return out
 

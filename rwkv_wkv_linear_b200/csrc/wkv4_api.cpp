@@ -7,6 +7,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/wkv4.h"
@@ -145,6 +146,33 @@ int cuda_status(cudaError_t e) {
     cudaGetLastError();
     return WKV4_ERR_CUDA;
 }
+
+// Whether any of `out` overlaps one of `in`, or another of `out`.
+template <size_t N, size_t M>
+bool any_overlap(const Range (&in)[N], const Range (&out)[M]) {
+    for (size_t i = 0; i < M; ++i) {
+        for (size_t j = 0; j < N; ++j)
+            if (overlap(out[i], in[j])) return true;
+        for (size_t j = i + 1; j < M; ++j)
+            if (overlap(out[i], out[j])) return true;
+    }
+    return false;
+}
+
+// Zero fill of the given rows (NULL entries skipped).
+int zero_rows(std::initializer_list<float*> rows, size_t bytes, cudaStream_t stream) {
+    for (float* p : rows) {
+        if (!p) continue;
+        const cudaError_t e = cudaMemsetAsync(p, 0, bytes, stream);
+        if (e != cudaSuccess) return cuda_status(e);
+    }
+    return WKV4_OK;
+}
+
+// A grid of a * b CTAs is launchable.
+bool fits_grid(int64_t a, int64_t b) { return a == 0 || b <= (int64_t)INT32_MAX / a; }
+
+constexpr int64_t kMaxBackwardSteps = 1ll << 24;
 
 int run_scan(const FwdArgs& a, bool want_tma) {
     return cuda_status(wkv4::launch_scan(a, want_tma && tma_eligible(a), encode_btc));
@@ -321,11 +349,100 @@ int wkv4_state_combine(int64_t B, int64_t C, const float* w, int64_t n_steps, co
     return cuda_status(wkv4::launch_state_combine(B, C, w, n_steps, x, y, out, (cudaStream_t)stream));
 }
 
+int wkv4_backward(int64_t B, int64_t T, int64_t C, const float* w, const float* u, const void* k,
+                  const void* v, const void* r, const float* state_in, const void* gy,
+                  const float* state_out, const float* gstate_out, void* gk, void* gv, void* gr,
+                  float* gw, float* gu, float* gstate_in, void* workspace, size_t workspace_bytes,
+                  wkv4_stream_t stream, int dtype) {
+    int rc = check_common(B, T, C, dtype);
+    if (rc != WKV4_OK) return rc;
+    if (C == 0) return WKV4_OK;
+    if (!gw || !gu) return WKV4_ERR_ARG;
+    if (B > 0 && (!w || (gstate_out && !state_out) || (gstate_in && !state_in))) return WKV4_ERR_ARG;
+    if (B > 0 && T > 0 && (!u || !k || !v || !gy || !gk || !gv || (r && !gr))) return WKV4_ERR_ARG;
+    if (T > kMaxBackwardSteps || !fits_grid(B, (C + 63) / 64 * 8)) return WKV4_ERR_ARG;
+    const size_t need = wkv4_backward_workspace(B, T, C, dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need || !is_aligned(workspace, 16)))
+        return WKV4_ERR_ARG;
+    const size_t es = wkv4::dtype_size(dtype);
+    const uint64_t io = (uint64_t)B * T * C * es, st = (uint64_t)3 * B * C * 4, row = (uint64_t)C * 4;
+    const Range in[] = {range_of(w, row),         range_of(u, row),
+                        range_of(k, io),          range_of(v, io),
+                        range_of(r, io),          range_of(gy, io),
+                        range_of(state_in, st),   range_of(gstate_out ? state_out : nullptr, st),
+                        range_of(gstate_out, st)};
+    const Range out[] = {range_of(gk, io),  range_of(gv, io),         range_of(r ? gr : nullptr, io),
+                         range_of(gw, row), range_of(gu, row),        range_of(gstate_in, st),
+                         range_of(need > 0 ? workspace : nullptr, need)};
+    if (any_overlap(in, out)) return WKV4_ERR_ALIAS;
+    if (B == 0)  // nothing to sum
+        return zero_rows({gw, gu}, row, (cudaStream_t)stream);
+    wkv4::BwdArgs a{B,  T,  C,  w,  u,  k,         v,         T > 0 ? r : nullptr,   gy,
+                    state_in, state_out, gstate_out, gk, gv, gr, gw, gu, gstate_in, workspace, dtype,
+                    (cudaStream_t)stream};
+    return cuda_status(wkv4::launch_backward(a));
+}
+
+size_t wkv4_backward_workspace(int64_t B, int64_t T, int64_t C, int dtype) {
+    if (B <= 0 || T < 0 || C <= 0 || check_common(B, T, C, dtype) != WKV4_OK) return 0;
+    return wkv4::backward_workspace(B, T, C, dtype);
+}
+
+int wkv4_token_shift_backward(int64_t B, int64_t T, int64_t C, const void* x, const void* x_prev,
+                              const float* mix_k, const float* mix_v, const float* mix_r,
+                              const void* gxk, const void* gxv, const void* gxr,
+                              const void* gx_last, void* gx, void* gx_prev, float* gmix_k,
+                              float* gmix_v, float* gmix_r, void* workspace,
+                              size_t workspace_bytes, wkv4_stream_t stream, int dtype) {
+    int rc = check_common(B, T, C, dtype);
+    if (rc != WKV4_OK) return rc;
+    if (C == 0) return WKV4_OK;
+    if (!gmix_k || !gmix_v || (mix_r && !gmix_r)) return WKV4_ERR_ARG;
+    if (B > 65535 || T > 65535ll * 16) return WKV4_ERR_ARG;
+    const bool rows = B > 0 && T > 0;
+    if (rows && (!x || !mix_k || !mix_v || !gxk || !gxv || (mix_r && !gxr) || !gx)) return WKV4_ERR_ARG;
+    const size_t need = wkv4_token_shift_backward_workspace(B, T, C, mix_r != nullptr);
+    if (need > 0 && (!workspace || workspace_bytes < need || !is_aligned(workspace, 16)))
+        return WKV4_ERR_ARG;
+    const size_t es = wkv4::dtype_size(dtype);
+    const uint64_t io = (uint64_t)B * T * C * es, one = (uint64_t)B * C * es, row = (uint64_t)C * 4;
+    const Range in[] = {range_of(x, io),      range_of(x_prev, one), range_of(mix_k, row),
+                        range_of(mix_v, row), range_of(mix_r, row),  range_of(gxk, io),
+                        range_of(gxv, io),    range_of(mix_r ? gxr : nullptr, io),
+                        range_of(gx_last, one)};
+    const Range out[] = {range_of(gx, io),      range_of(gx_prev, one), range_of(gmix_k, row),
+                         range_of(gmix_v, row), range_of(mix_r ? gmix_r : nullptr, row),
+                         range_of(need > 0 ? workspace : nullptr, need)};
+    if (any_overlap(in, out)) return WKV4_ERR_ALIAS;
+    if (!rows) {
+        cudaStream_t s = (cudaStream_t)stream;
+        if (gx_prev && one > 0) {  // x_last is x_prev when T == 0
+            const cudaError_t e = gx_last ? cudaMemcpyAsync(gx_prev, gx_last, one, cudaMemcpyDeviceToDevice, s)
+                                          : cudaMemsetAsync(gx_prev, 0, one, s);
+            if (e != cudaSuccess) return cuda_status(e);
+        }
+        return zero_rows({gmix_k, gmix_v, mix_r ? gmix_r : nullptr}, row, s);
+    }
+    wkv4::ShiftBwdArgs a{B, T, C, x, x_prev, {mix_k, mix_v, mix_r}, {gxk, gxv, mix_r ? gxr : nullptr},
+                         gx_last, gx, gx_prev, {gmix_k, gmix_v, mix_r ? gmix_r : nullptr},
+                         workspace, dtype, (cudaStream_t)stream};
+    return cuda_status(wkv4::launch_shift_backward(a));
+}
+
+size_t wkv4_token_shift_backward_workspace(int64_t B, int64_t T, int64_t C, int with_r) {
+    if (B <= 0 || T <= 0 || C <= 0) return 0;
+    return wkv4::shift_backward_workspace(B, T, C, with_r ? 3 : 2);
+}
+
 int wkv4_device_error(int reset) {
     unsigned bits = 0;
-    if (wkv4::read_device_error(&bits, reset != 0) != cudaSuccess) {
-        cudaGetLastError();
-        return WKV4_ERR_CUDA;
+    for (auto read : {wkv4::read_device_error, wkv4::read_train_error}) {
+        unsigned word = 0;
+        if (read(&word, reset != 0) != cudaSuccess) {
+            cudaGetLastError();
+            return WKV4_ERR_CUDA;
+        }
+        bits |= word;
     }
     if (bits & (wkv4::kErrTmaWait | wkv4::kErrExchangeWait)) return WKV4_ERR_TIMEOUT;
     return bits ? WKV4_ERR_SLOT : WKV4_OK;

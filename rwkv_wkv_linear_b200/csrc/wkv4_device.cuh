@@ -33,9 +33,10 @@
 
 namespace wkv4 {
 
-// The device error word (per device; wkv4_device_error reads and clears it):
-// the bits of wkv4_internal.h, set by the kernels with atomicOr.
-__device__ unsigned int g_device_error = 0;
+// The device error word (per device and translation unit; wkv4_device_error
+// reads and clears them all): the bits of wkv4_internal.h, set by the kernels
+// with atomicOr.
+static __device__ unsigned int g_device_error = 0;
 
 // Checked builds (WKV4_CHECKED): every global index is checked against the
 // extent of its buffer before the access; one outside it sets kErrBounds in

@@ -72,7 +72,52 @@ cudaError_t launch_copy_state(const FwdArgs& a);  // T == 0
 cudaError_t launch_state_combine(int64_t B, int64_t C, const float* w, int64_t n, const float* x,
                                  const float* y, float* out, cudaStream_t stream);
 
-// Device error word of the current device (synchronous read; optional reset).
-cudaError_t read_device_error(unsigned* bits, bool reset);
+// Backward pass of the (gated) recurrence.
+struct BwdArgs {
+    int64_t B, T, C;
+    const float* w;
+    const float* u;
+    const void* k;
+    const void* v;
+    const void* r;  // NULL: no gate
+    const void* gy;
+    const float* state_in;
+    const float* state_out;
+    const float* gstate_out;
+    void* gk;
+    void* gv;
+    void* gr;
+    float* gw;
+    float* gu;
+    float* gstate_in;
+    void* workspace;
+    int dtype;
+    cudaStream_t stream;
+};
+cudaError_t launch_backward(const BwdArgs& a);  // T >= 0, B, C >= 1
+size_t backward_workspace(int64_t B, int64_t T, int64_t C, int dtype);
+
+// Backward pass of the token shift (two mixes, or three).
+struct ShiftBwdArgs {
+    int64_t B, T, C;
+    const void* x;
+    const void* x_prev;
+    const float* mix[3];
+    const void* g[3];
+    const void* gx_last;
+    void* gx;
+    void* gx_prev;
+    float* gmix[3];
+    void* workspace;
+    int dtype;
+    cudaStream_t stream;
+};
+cudaError_t launch_shift_backward(const ShiftBwdArgs& a);  // T, B, C >= 1
+size_t shift_backward_workspace(int64_t B, int64_t T, int64_t C, int n);
+
+// Device error words of the current device, one a translation unit with
+// kernels (synchronous read; optional reset).
+cudaError_t read_device_error(unsigned* bits, bool reset);  // wkv4_kernels.cu
+cudaError_t read_train_error(unsigned* bits, bool reset);   // wkv4_train.cu
 
 }  // namespace wkv4

@@ -31,6 +31,7 @@
 #include "../../include/wkv4.h"
 #include "wkv4_device.cuh"
 #include "wkv4_internal.h"
+#include "wkv4_launch.cuh"
 #include "wkv4_scan.cuh"
 #include "wkv4_seq.cuh"
 #include "wkv4_shift.cuh"
@@ -46,23 +47,6 @@ namespace wkv4 {
 
 size_t dtype_size(int dtype) { return dtype == WKV4_F32 ? 4 : 2; }
 
-// The dynamic shared memory limit is a per-device function attribute: set it
-// once per device for each kernel instantiation.
-struct DeviceFlags {
-    std::atomic<bool> done[64];
-};
-
-template <typename Kern>
-static cudaError_t ensure_smem_attr(DeviceFlags& f, Kern kern, size_t smem) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64 && f.done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && dev >= 0 && dev < 64) f.done[dev].store(true, std::memory_order_release);
-    return e;
-}
-
 template <typename IO, int L, int NW, int NS>
 static Geom seq_geom_t() {
     using Sh = SeqShape<IO, L, NW, NS>;
@@ -75,63 +59,8 @@ Geom seq_geom(int dtype) {
     return seq_geom_t<WKV4_SEQ_BF16>();
 }
 
-static int env_int(const char* name, int dflt) {
-    const char* e = std::getenv(name);
-    return e ? std::atoi(e) : dflt;
-}
-
 constexpr size_t kMaxSmem = 227 * 1024;
 constexpr int kTmemColumns = 512;  // tensor-memory columns per SM
-constexpr int kMaxDevices = 64;
-
-// Per-device limits the launch shapes are worked out from, queried once per
-// device (the launchers run on every call; attribute queries are not free).
-struct DeviceAttrs {
-    int smem_per_sm = 233472, smem_reserved = 1024, reg_file = 65536, max_threads = 2048,
-        max_blocks = 32, sms = 148;
-};
-
-static const DeviceAttrs& device_attrs() {
-    static DeviceAttrs attrs[kMaxDevices];
-    static std::once_flag once[kMaxDevices];
-    static DeviceAttrs fallback;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-        cudaGetLastError();
-        return fallback;
-    }
-    std::call_once(once[dev], [dev] {
-        DeviceAttrs& a = attrs[dev];
-        cudaDeviceGetAttribute(&a.smem_per_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
-        cudaDeviceGetAttribute(&a.smem_reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev);
-        cudaDeviceGetAttribute(&a.reg_file, cudaDevAttrMaxRegistersPerMultiprocessor, dev);
-        cudaDeviceGetAttribute(&a.max_threads, cudaDevAttrMaxThreadsPerMultiProcessor, dev);
-        cudaDeviceGetAttribute(&a.max_blocks, cudaDevAttrMaxBlocksPerMultiprocessor, dev);
-        cudaDeviceGetAttribute(&a.sms, cudaDevAttrMultiProcessorCount, dev);
-        cudaGetLastError();
-    });
-    return attrs[dev];
-}
-
-// A launch that may begin while the kernel before it in the stream is
-// finishing (programmatic stream serialization): every kernel of the library
-// waits for the earlier grid before its first global access.
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                              cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t cfg;
-    std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
 
 // Tuning overrides of the scan's launch shape, read from the environment
 // once per process: WKV4_SCAN_NW (warps per CTA), WKV4_SCAN_CLUSTER (cluster
@@ -139,60 +68,6 @@ static cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 struct ScanOverrides {
     int nw, nc, waves;
 };
-
-// Limit of each bounded device-side wait, in rounds of about 1 ms.  Checked
-// builds (WKV4_CHECKED) take WKV4_WAIT_ROUNDS from the environment, so that a
-// test can make a wait run out quickly.
-static uint32_t wait_rounds() {
-#ifdef WKV4_CHECKED
-    static const int r = env_int("WKV4_WAIT_ROUNDS", 0);
-    if (r > 0) return (uint32_t)r;
-#endif
-    return kWaitRounds;
-}
-
-// Fault injection, in checked builds only (WKV4_CHECKED), read once from
-// WKV4_FAULT:
-//   launch:N   the N-th kernel launch of the process (1-based) is made with an
-//              empty grid, which the runtime rejects (cudaErrorInvalid-
-//              Configuration) without running anything: the launch error path
-//              of every entry point, with no GPU fault;
-//   exchange   no scan CTA pushes its segment aggregate, so every CTA's
-//              bounded wait for its peers' aggregates runs out (with a short
-//              limit from WKV4_WAIT_ROUNDS): the expiry path of the exchange.
-// Production builds compile none of it.
-struct FaultPlan {
-    long launch_at = 0;  // 0: none
-    bool exchange = false;
-};
-
-static const FaultPlan& fault_plan() {
-    static const FaultPlan plan = [] {
-        FaultPlan f;
-#ifdef WKV4_CHECKED
-        if (const char* e = std::getenv("WKV4_FAULT")) {
-            if (std::strncmp(e, "launch:", 7) == 0) f.launch_at = std::atol(e + 7);
-            if (std::strcmp(e, "exchange") == 0) f.exchange = true;
-        }
-#endif
-        return f;
-    }();
-    return plan;
-}
-
-// The grid of a launch: `g`, or an empty grid for the launch fault injection
-// picks (one count over every launcher of the process).
-#ifdef WKV4_CHECKED
-static std::atomic<long> g_launches{0};
-#endif
-template <typename G>
-static G launch_grid(G g) {
-#ifdef WKV4_CHECKED
-    const long at = fault_plan().launch_at;
-    if (at > 0 && g_launches.fetch_add(1) + 1 == at) return G(0);
-#endif
-    return g;
-}
 
 static const ScanOverrides& scan_overrides() {
     static const ScanOverrides o{env_int("WKV4_SCAN_NW", 0), env_int("WKV4_SCAN_CLUSTER", 0),
@@ -572,10 +447,6 @@ cudaError_t launch_step(const FwdArgs& a) {
     return cudaGetLastError();
 }
 
-static bool aligned(const void* ptr, size_t bytes) {
-    return ptr == nullptr || ((uintptr_t)ptr % bytes) == 0;
-}
-
 // (kSlots: the slot-indexed decode, which has no gate)
 template <typename IO, int V, bool kSlots = false>
 static void launch_decode_io(const FwdArgs& a, const StepParams& p, unsigned grid) {
@@ -719,16 +590,6 @@ cudaError_t launch_state_combine(int64_t B, int64_t C, const float* w, int64_t n
     return cudaGetLastError();
 }
 
-cudaError_t read_device_error(unsigned* bits, bool reset) {
-    cudaError_t e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyFromSymbol(bits, g_device_error, sizeof(unsigned));
-    if (e != cudaSuccess) return e;
-    if (reset) {
-        const unsigned zero = 0;
-        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof(unsigned));
-    }
-    return e;
-}
+cudaError_t read_device_error(unsigned* bits, bool reset) { return read_error_word(bits, reset); }
 
 }  // namespace wkv4

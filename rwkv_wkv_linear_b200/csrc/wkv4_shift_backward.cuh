@@ -1,0 +1,139 @@
+// Backward pass of the token shift.  Forward, for up to three mixes m_i,
+//   out_i[b,t] = m_i x[b,t] + (1 - m_i) x[b,t-1],  x[b,-1] = x_prev[b],
+// so with g_i the gradient of out_i
+//   gx[b,t]    = sum_i m_i g_i[b,t] + sum_i (1 - m_i) g_i[b,t+1]   (t + 1 < T)
+//              (+ gx_last[b] at t = T - 1: x_last = x[:, T-1] feeds the next call),
+//   gx_prev[b] = sum_i (1 - m_i) g_i[b,0],
+//   gm_i       = sum_{b,t} g_i[b,t] (x[b,t] - x[b,t-1]).
+//
+// An HBM stream like the forward: a thread owns V channels of one batch row
+// and walks a run of steps with the row before in registers (x[t-1], and
+// sum_i m_i g_i[t-1], which waits for the next row's share before it is
+// stored), so every input is read once (plus one row a run) and gx written
+// once.  The gm_i partial sums of the CTA's runs are joined in shared memory
+// and written one row a CTA; wkv4_column_sum_kernel adds the rows in a fixed
+// order.  All arithmetic in fp32, rounded once at the stores.
+#pragma once
+
+#include "wkv4_device.cuh"
+#include "wkv4_shift.cuh"  // load_f32
+
+namespace wkv4 {
+
+struct ShiftBwdParams {
+    int64_t B, T, C;
+    const void* x;
+    const void* x_prev;   // [B][C] or NULL (zero)
+    const float* mix[3];
+    const void* g[3];     // gradients of the outputs
+    const void* gx_last;  // [B][C] or NULL
+    void* gx;
+    void* gx_prev;        // [B][C] or NULL
+    float* part;          // [n][rows][C] partial sums of gm, row (b, y block)
+    int64_t rows;
+    int64_t run;          // steps a thread walks
+};
+
+constexpr int kShiftBwdX = 32;  // channel groups a CTA
+constexpr int kShiftBwdY = 4;   // runs a CTA
+
+template <typename IO, int V, int N>
+__global__ void __launch_bounds__(kShiftBwdX* kShiftBwdY)
+    wkv4_token_shift_backward_kernel(const ShiftBwdParams p) {
+    allow_dependents();
+    grid_dependency_wait();
+    const int64_t b = blockIdx.z;
+    const int64_t c = ((int64_t)blockIdx.x * kShiftBwdX + threadIdx.x) * V;
+    const int64_t t0 = ((int64_t)blockIdx.y * kShiftBwdY + threadIdx.y) * p.run;
+    const int64_t t1 = min(p.T, t0 + p.run);
+    __shared__ float red[N][kShiftBwdY][kShiftBwdX * V];
+    float acc[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[i][j] = 0.f;
+    if (c < p.C && t0 < t1 && in_range(c + V - 1, p.C) && in_range(b, p.B)) {
+        const int64_t row = b * p.T;
+        const IO* x = static_cast<const IO*>(p.x);
+        float m[N][V], xp[V], a[V];
+#pragma unroll
+        for (int i = 0; i < N; ++i) load_f32<V>(p.mix[i] + c, m[i]);
+#pragma unroll
+        for (int j = 0; j < V; ++j) xp[j] = a[j] = 0.f;
+        if (t0 > 0) {
+            load_vec<IO, V>(x + (row + t0 - 1) * p.C + c, xp);
+        } else if (p.x_prev) {
+            load_vec<IO, V>(static_cast<const IO*>(p.x_prev) + b * p.C + c, xp);
+        }
+        // row t's shares: own[j] = sum m g to gx[t], prev[j] = sum (1 - m) g to gx[t - 1]
+        auto row_grads = [&](const float (&g)[N][V], float (&own)[V], float (&prev)[V]) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                own[j] = m[0][j] * g[0][j];
+                prev[j] = fmaf(-m[0][j], g[0][j], g[0][j]);
+#pragma unroll
+                for (int i = 1; i < N; ++i) {
+                    own[j] = fmaf(m[i][j], g[i][j], own[j]);
+                    prev[j] += fmaf(-m[i][j], g[i][j], g[i][j]);
+                }
+            }
+        };
+        auto store_gx = [&](int64_t t, const float (&o)[V]) {
+            store_vec<IO, V>(static_cast<IO*>(p.gx) + (row + t) * p.C + c, o);
+        };
+#pragma unroll 4
+        for (int64_t t = t0; t < t1; ++t) {
+            const int64_t off = (row + t) * p.C + c;
+            float xt[V], g[N][V], own[V], prev[V];
+            load_vec<IO, V>(x + off, xt);
+#pragma unroll
+            for (int i = 0; i < N; ++i) load_vec<IO, V>(static_cast<const IO*>(p.g[i]) + off, g[i]);
+            row_grads(g, own, prev);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i][j] = fmaf(g[i][j], xt[j] - xp[j], acc[i][j]);
+                xp[j] = xt[j];
+                a[j] += prev[j];
+            }
+            if (t > t0) {
+                store_gx(t - 1, a);
+            } else if (t == 0 && p.gx_prev) {
+                store_vec<IO, V>(static_cast<IO*>(p.gx_prev) + b * p.C + c, prev);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) a[j] = own[j];
+        }
+        // the run's last row takes its share of the row after it
+        if (t1 < p.T) {
+            const int64_t off = (row + t1) * p.C + c;
+            float g[N][V], own[V], prev[V];
+#pragma unroll
+            for (int i = 0; i < N; ++i) load_vec<IO, V>(static_cast<const IO*>(p.g[i]) + off, g[i]);
+            row_grads(g, own, prev);
+#pragma unroll
+            for (int j = 0; j < V; ++j) a[j] += prev[j];
+        } else if (p.gx_last) {
+            float gl[V];
+            load_vec<IO, V>(static_cast<const IO*>(p.gx_last) + b * p.C + c, gl);
+#pragma unroll
+            for (int j = 0; j < V; ++j) a[j] += gl[j];
+        }
+        store_gx(t1 - 1, a);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) red[i][threadIdx.y][j * kShiftBwdX + threadIdx.x] = acc[i][j];
+    __syncthreads();
+    const int64_t prow = b * gridDim.y + blockIdx.y;
+    for (int q = threadIdx.y; q < N * V; q += kShiftBwdY) {
+        const int i = q / V, j = q % V;
+        float s = 0.f;
+#pragma unroll
+        for (int y = 0; y < kShiftBwdY; ++y) s += red[i][y][j * kShiftBwdX + threadIdx.x];
+        if (c + j < p.C) p.part[(i * p.rows + prow) * p.C + c + j] = s;
+    }
+}
+
+}  // namespace wkv4

@@ -1,0 +1,222 @@
+// Launchers of the backward kernels: the WKV recurrence's (wkv4_backward.cuh)
+// and the token shift's (wkv4_shift_backward.cuh).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/wkv4.h"
+#include "wkv4_backward.cuh"
+#include "wkv4_launch.cuh"
+#include "wkv4_shift_backward.cuh"
+
+namespace wkv4 {
+
+// Launch shape of the backward pass, from T and the type alone (the workspace
+// is sized from it): warps a CTA, CTAs a cluster, rounds.
+struct BwdShape {
+    int NW, NC;
+    int64_t rounds;
+};
+
+static BwdShape bwd_shape(int64_t T, int dtype) {
+    BwdShape s;
+    s.NW = dtype == WKV4_F32 || T <= 4 * kBwdL ? 4 : 8;
+    const int64_t ctas = std::max<int64_t>(1, (T + s.NW * kBwdL - 1) / (s.NW * kBwdL));
+    s.NC = 1;
+    while (s.NC < 8 && s.NC < ctas) s.NC *= 2;
+    s.rounds = (ctas + s.NC - 1) / s.NC;
+    return s;
+}
+
+// Workspace: partial sums of gw, gu (one row a CTA of each cluster, none when
+// one CTA a channel tile writes them itself), then the rounds' states.
+static size_t align16(size_t n) { return (n + 15) & ~(size_t)15; }
+static size_t bwd_part_bytes(int64_t B, int64_t C, const BwdShape& s) {
+    return B * s.NC == 1 ? 0 : align16((size_t)2 * B * s.NC * C * 4);
+}
+
+size_t backward_workspace(int64_t B, int64_t T, int64_t C, int dtype) {
+    const BwdShape s = bwd_shape(T, dtype);
+    return bwd_part_bytes(B, C, s) + (s.rounds > 1 ? (size_t)s.rounds * B * C * 16 : 0);
+}
+
+static cudaError_t launch_column_sum(const float* part, float* o0, float* o1, float* o2, int n,
+                                     int64_t rows, int64_t C, cudaStream_t stream) {
+    const ColumnSumParams p{part, {o0, o1, o2}, rows, C};
+    return launch_pdl(wkv4_column_sum_kernel, launch_grid(dim3((unsigned)((C + 31) / 32), (unsigned)n)),
+                      dim3(256), 0, stream, p);
+}
+
+template <typename IO, bool kGate>
+static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdShape& sh) {
+    const BwdLayout<IO> lay{sh.NW};
+    auto kern = wkv4_backward_kernel<IO, kGate>;
+    static DeviceFlags attr;
+    cudaError_t e = ensure_smem_attr(attr, kern, BwdLayout<IO>{8}.bytes());
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = a.B * p.CGB;
+    if (sh.rounds > 1) {
+        auto sum = wkv4_backward_summary_kernel<IO>;
+        const size_t smem = (size_t)sh.NW * (4 * BwdLayout<IO>::kTile + kBwdC * 16);
+        static DeviceFlags sattr;
+        e = ensure_smem_attr(sattr, sum, (size_t)8 * (4 * BwdLayout<IO>::kTile + kBwdC * 16));
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(sum, launch_grid(dim3((unsigned)tiles, (unsigned)sh.rounds)), dim3(32 * sh.NW),
+                       smem, a.stream, p, sh.NC);
+        if (e != cudaSuccess) return e;
+        const int64_t BC = a.B * a.C;
+        e = launch_pdl(wkv4_backward_prefix_kernel, launch_grid(dim3((unsigned)((BC + 127) / 128))),
+                       dim3(128), 0, a.stream, p, (int64_t)sh.NC * sh.NW * kBwdL);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = launch_grid(dim3((unsigned)(tiles * sh.NC)));
+    cfg.blockDim = dim3(32 * sh.NW);
+    cfg.dynamicSmemBytes = lay.bytes();
+    cfg.stream = a.stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)sh.NC;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, p);
+    if (e != cudaSuccess) return e;
+    if (a.B * sh.NC > 1)
+        e = launch_column_sum(p.part_w, a.gw, a.gu, nullptr, 2, a.B * sh.NC, a.C, a.stream);
+    return e;
+}
+
+cudaError_t launch_backward(const BwdArgs& a) {
+    const BwdShape sh = bwd_shape(a.T, a.dtype);
+    BwdParams p{};
+    p.B = a.B;
+    p.T = a.T;
+    p.C = a.C;
+    p.CGB = (int)((a.C + kBwdC - 1) / kBwdC);
+    p.rounds = (int)sh.rounds;
+    p.w = a.w;
+    p.u = a.u;
+    p.k = a.k;
+    p.v = a.v;
+    p.r = a.r;
+    p.gy = a.gy;
+    p.state_in = a.state_in;
+    p.state_out = a.state_out;
+    p.gstate_out = a.gstate_out;
+    p.gk = a.gk;
+    p.gv = a.gv;
+    p.gr = a.gr;
+    p.gstate_in = a.gstate_in;
+    unsigned char* ws = static_cast<unsigned char*>(a.workspace);
+    if (a.B * sh.NC > 1) {
+        p.part_w = reinterpret_cast<float*>(ws);
+        p.part_u = p.part_w + a.B * sh.NC * a.C;
+        ws += bwd_part_bytes(a.B, a.C, sh);
+    } else {
+        p.part_w = a.gw;
+        p.part_u = a.gu;
+    }
+    if (sh.rounds > 1) {
+        const int64_t n = sh.rounds * a.B * a.C;
+        p.ck_p = reinterpret_cast<double*>(ws);
+        p.ck_a = reinterpret_cast<float*>(ws + n * 8);
+        p.ck_b = p.ck_a + n;
+    }
+    const size_t es = dtype_size(a.dtype);
+    p.vec_load = (a.C * es) % 16 == 0 && aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.gy, 16) &&
+                 aligned(a.r, 16);
+    p.vec_store = a.C % 2 == 0 && aligned(a.gk, 2 * es) && aligned(a.gv, 2 * es) && aligned(a.gr, 2 * es);
+    switch (a.dtype) {
+        case WKV4_F32:
+            return a.r ? launch_backward_t<float, true>(a, p, sh) : launch_backward_t<float, false>(a, p, sh);
+        case WKV4_F16:
+            return a.r ? launch_backward_t<__half, true>(a, p, sh) : launch_backward_t<__half, false>(a, p, sh);
+        default:
+            return a.r ? launch_backward_t<__nv_bfloat16, true>(a, p, sh)
+                       : launch_backward_t<__nv_bfloat16, false>(a, p, sh);
+    }
+}
+
+// ------------------------------------------------------------- token shift
+
+// Runs of the token shift's backward pass: as many CTAs as the GPU holds at
+// once (8 of 128 threads an SM), at least kShiftMinRun steps a run.
+struct ShiftBwdShape {
+    int V;
+    int64_t run, yblocks;
+};
+
+static ShiftBwdShape shift_bwd_shape(int64_t B, int64_t T, int64_t C, bool vec) {
+    ShiftBwdShape s;
+    s.V = vec ? 4 : 1;
+    const int64_t xb = (C + kShiftBwdX * s.V - 1) / (kShiftBwdX * s.V);
+    const int64_t blocks = std::max<int64_t>(1, (int64_t)148 * 8 / std::max<int64_t>(1, xb * B));
+    const int64_t runs = blocks * kShiftBwdY;
+    s.run = std::max<int64_t>((T + runs - 1) / runs, kShiftMinRun);
+    s.run = std::max<int64_t>(s.run, (T + 65535ll * kShiftBwdY - 1) / (65535ll * kShiftBwdY));
+    s.yblocks = (T + s.run * kShiftBwdY - 1) / (s.run * kShiftBwdY);
+    return s;
+}
+
+size_t shift_backward_workspace(int64_t B, int64_t T, int64_t C, int n) {
+    // either channel width may be taken (it depends on the pointers' alignment)
+    const int64_t rows = std::max(shift_bwd_shape(B, T, C, true).yblocks, shift_bwd_shape(B, T, C, false).yblocks);
+    return (size_t)n * B * rows * C * 4;
+}
+
+template <typename IO, int V, int N>
+static cudaError_t launch_shift_bwd_t(const ShiftBwdParams& p, const ShiftBwdShape& s, cudaStream_t stream) {
+    const dim3 grid((unsigned)((p.C + kShiftBwdX * V - 1) / (kShiftBwdX * V)), (unsigned)s.yblocks, (unsigned)p.B);
+    return launch_pdl(wkv4_token_shift_backward_kernel<IO, V, N>, launch_grid(grid),
+                      dim3(kShiftBwdX, kShiftBwdY), 0, stream, p);
+}
+
+template <typename IO>
+static cudaError_t launch_shift_bwd_io(const ShiftBwdParams& p, const ShiftBwdShape& s, int n,
+                                       cudaStream_t stream) {
+    if (n == 3)
+        return s.V == 4 ? launch_shift_bwd_t<IO, 4, 3>(p, s, stream) : launch_shift_bwd_t<IO, 1, 3>(p, s, stream);
+    return s.V == 4 ? launch_shift_bwd_t<IO, 4, 2>(p, s, stream) : launch_shift_bwd_t<IO, 1, 2>(p, s, stream);
+}
+
+cudaError_t launch_shift_backward(const ShiftBwdArgs& a) {
+    const int n = a.mix[2] ? 3 : 2;
+    const size_t es = dtype_size(a.dtype);
+    bool vec = a.C % 4 == 0 && aligned(a.x, 4 * es) && aligned(a.x_prev, 4 * es) &&
+               aligned(a.gx, 4 * es) && aligned(a.gx_prev, 4 * es) && aligned(a.gx_last, 4 * es);
+    for (int i = 0; i < n; ++i) vec = vec && aligned(a.mix[i], 16) && aligned(a.g[i], 4 * es);
+    const ShiftBwdShape s = shift_bwd_shape(a.B, a.T, a.C, vec);
+    ShiftBwdParams p{};
+    p.B = a.B;
+    p.T = a.T;
+    p.C = a.C;
+    p.x = a.x;
+    p.x_prev = a.x_prev;
+    p.gx_last = a.gx_last;
+    p.gx = a.gx;
+    p.gx_prev = a.gx_prev;
+    for (int i = 0; i < n; ++i) {
+        p.mix[i] = a.mix[i];
+        p.g[i] = a.g[i];
+    }
+    p.part = static_cast<float*>(a.workspace);
+    p.rows = a.B * s.yblocks;
+    p.run = s.run;
+    cudaError_t e;
+    switch (a.dtype) {
+        case WKV4_F32: e = launch_shift_bwd_io<float>(p, s, n, a.stream); break;
+        case WKV4_F16: e = launch_shift_bwd_io<__half>(p, s, n, a.stream); break;
+        default: e = launch_shift_bwd_io<__nv_bfloat16>(p, s, n, a.stream); break;
+    }
+    if (e != cudaSuccess) return e;
+    return launch_column_sum(p.part, a.gmix[0], a.gmix[1], a.gmix[2], n, p.rows, a.C, a.stream);
+}
+
+cudaError_t read_train_error(unsigned* bits, bool reset) { return read_error_word(bits, reset); }
+
+}  // namespace wkv4

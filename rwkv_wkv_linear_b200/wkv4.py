@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -26,11 +26,11 @@ STATUS = {0: "OK", -1: "ERR_ARG", -2: "ERR_DTYPE", -3: "ERR_ALIAS", -4: "ERR_CUD
 
 _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
-EXPORTS = ("wkv4_decode_step", "wkv4_decode_step_gated", "wkv4_decode_step_slots",
+EXPORTS = ("wkv4_backward", "wkv4_backward_workspace", "wkv4_decode_step", "wkv4_decode_step_gated", "wkv4_decode_step_slots",
            "wkv4_device_error", "wkv4_forward", "wkv4_forward_gated", "wkv4_forward_gated_variant",
            "wkv4_forward_host", "wkv4_forward_host_workspace",
            "wkv4_forward_variant", "wkv4_state_combine", "wkv4_status_string", "wkv4_token_shift",
-           "wkv4_version")
+           "wkv4_token_shift_backward", "wkv4_token_shift_backward_workspace", "wkv4_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -77,6 +77,15 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.wkv4_decode_step_slots.restype = i32
             lib.wkv4_token_shift.argtypes = [i64, i64, i64] + [vp] * 10 + [i32]
             lib.wkv4_token_shift.restype = i32
+            lib.wkv4_backward.argtypes = [i64] * 3 + [vp] * 16 + [ctypes.c_size_t, vp, i32]
+            lib.wkv4_backward.restype = i32
+            lib.wkv4_backward_workspace.argtypes = [i64, i64, i64, i32]
+            lib.wkv4_backward_workspace.restype = ctypes.c_size_t
+            lib.wkv4_token_shift_backward.argtypes = ([i64] * 3 + [vp] * 15
+                                                      + [ctypes.c_size_t, vp, i32])
+            lib.wkv4_token_shift_backward.restype = i32
+            lib.wkv4_token_shift_backward_workspace.argtypes = [i64, i64, i64, i32]
+            lib.wkv4_token_shift_backward_workspace.restype = ctypes.c_size_t
             lib.wkv4_device_error.argtypes = [i32]
             lib.wkv4_device_error.restype = i32
             lib.wkv4_status_string.argtypes = [i32]
@@ -430,6 +439,148 @@ def state_combine(x: Optional[torch.Tensor], y: torch.Tensor, n_steps: int, w: t
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_state_combine")
     return out
+
+
+class Grads(NamedTuple):
+    """Gradients of a forward call (gr: gated only; gstate_in: with a state_in only)."""
+    gk: torch.Tensor
+    gv: torch.Tensor
+    gr: Optional[torch.Tensor]
+    gw: torch.Tensor
+    gu: torch.Tensor
+    gstate_in: Optional[torch.Tensor]
+
+
+class ShiftGrads(NamedTuple):
+    """Gradients of a token shift call (gmix_r: with mix_r only; gx_prev: with x_prev only)."""
+    gx: torch.Tensor
+    gmix_k: torch.Tensor
+    gmix_v: torch.Tensor
+    gmix_r: Optional[torch.Tensor]
+    gx_prev: Optional[torch.Tensor]
+
+
+def _workspace(given: Optional[torch.Tensor], need: int, dev: torch.device, stream):
+    """The call's workspace: the caller's, or a new one.  A new one is dropped
+    when the call returns, so the allocator is told which stream still uses it."""
+    if given is not None:
+        if given.dtype != torch.uint8:
+            raise ValueError("workspace must be uint8")
+        _check_dev("workspace", given)
+        return given
+    if need == 0:
+        return None
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            stream = torch.cuda.ExternalStream(raw, device=dev)
+        ws.record_stream(stream)
+    return ws
+
+
+def backward(k: torch.Tensor, v: torch.Tensor, w: torch.Tensor, u: torch.Tensor, gy: torch.Tensor,
+             state_in: Optional[torch.Tensor] = None, *, r: Optional[torch.Tensor] = None,
+             state_out: Optional[torch.Tensor] = None, gstate_out: Optional[torch.Tensor] = None,
+             workspace: Optional[torch.Tensor] = None, stream=None) -> Grads:
+    """wkv4_backward: the gradients of forward(k, v, w, u, state_in), or with r
+    of forward_gated, from gy [B, T, C] (the gradient of y) and, when the
+    returned state was used, gstate_out [3, B, C] with that state_out.  k, v,
+    r, gy [B, T, C] of one dtype; w, u [C] fp32; states [3, B, C] fp32.
+    workspace: CUDA uint8, at least backward_workspace_bytes(...) (allocated
+    when None)."""
+    if k.dim() != 3 or v.shape != k.shape or gy.shape != k.shape or (r is not None and r.shape != k.shape):
+        raise ValueError("k, v, gy (and r) must all be [B, T, C]")
+    B, T, C = k.shape
+    dt = _DTYPES.get(k.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {k.dtype}")
+    for name, t in (("k", k), ("v", v), ("gy", gy), ("r", r)):
+        _check_dev(name, t, k.dtype)
+    for name, t in (("w", w), ("u", u)):
+        _check_dev(name, t, torch.float32)
+        if t.shape != (C,):
+            raise ValueError(f"{name} must be [C]")
+    for name, t in (("state_in", state_in), ("state_out", state_out), ("gstate_out", gstate_out)):
+        _check_dev(name, t, torch.float32)
+        if t is not None and t.shape != (3, B, C):
+            raise ValueError(f"{name} must be [3, B, C]")
+    if gstate_out is not None and state_out is None:
+        raise ValueError("gstate_out needs the state_out it is the gradient of")
+    dev = _one_device(k=k, v=v, w=w, u=u, gy=gy, r=r, state_in=state_in, state_out=state_out,
+                      gstate_out=gstate_out, workspace=workspace)
+    with torch.cuda.device(dev):
+        gk, gv = torch.empty_like(k), torch.empty_like(v)
+        gr = torch.empty_like(r) if r is not None else None
+        gw, gu = torch.empty_like(w), torch.empty_like(u)
+        gs = torch.empty_like(state_in) if state_in is not None else None
+        ws = _workspace(workspace, load().wkv4_backward_workspace(B, T, C, dt), dev, stream)
+        rc = load().wkv4_backward(B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r),
+                                  _ptr(state_in), _ptr(gy), _ptr(state_out), _ptr(gstate_out),
+                                  _ptr(gk), _ptr(gv), _ptr(gr), _ptr(gw), _ptr(gu), _ptr(gs),
+                                  _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev), dt)
+    if rc != 0:
+        raise Wkv4Error(rc, "wkv4_backward")
+    return Grads(gk, gv, gr, gw, gu, gs)
+
+
+def backward_workspace_bytes(B: int, T: int, C: int, dtype: torch.dtype) -> int:
+    """wkv4_backward_workspace: device bytes backward needs."""
+    return int(load().wkv4_backward_workspace(B, T, C, _DTYPES[dtype]))
+
+
+def token_shift_backward(x: torch.Tensor, mix_k: torch.Tensor, mix_v: torch.Tensor,
+                         gxk: torch.Tensor, gxv: torch.Tensor,
+                         mix_r: Optional[torch.Tensor] = None, gxr: Optional[torch.Tensor] = None,
+                         x_prev: Optional[torch.Tensor] = None, *,
+                         gx_last: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> ShiftGrads:
+    """wkv4_token_shift_backward: the gradients of token_shift(x, mix_k, mix_v,
+    mix_r, x_prev) from those of its outputs (gxr with mix_r) and, when x_last
+    was used, of x_last [B, C].  workspace: CUDA uint8, at least
+    token_shift_backward_workspace_bytes(...) (allocated when None)."""
+    if x.dim() != 3:
+        raise ValueError("x must be [B, T, C]")
+    if (mix_r is None) != (gxr is None):
+        raise ValueError("mix_r and gxr go together")
+    B, T, C = x.shape
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    for name, t in (("x", x), ("gxk", gxk), ("gxv", gxv), ("gxr", gxr)):
+        _check_dev(name, t, x.dtype)
+        if t is not None and t.shape != x.shape:
+            raise ValueError(f"{name} must be [B, T, C]")
+    for name, m in (("mix_k", mix_k), ("mix_v", mix_v), ("mix_r", mix_r)):
+        _check_dev(name, m, torch.float32)
+        if m is not None and m.shape != (C,):
+            raise ValueError(f"{name} must be [C]")
+    for name, t in (("x_prev", x_prev), ("gx_last", gx_last)):
+        _check_dev(name, t, x.dtype)
+        if t is not None and t.shape != (B, C):
+            raise ValueError(f"{name} must be [B, C]")
+    dev = _one_device(x=x, mix_k=mix_k, mix_v=mix_v, mix_r=mix_r, gxk=gxk, gxv=gxv, gxr=gxr,
+                      x_prev=x_prev, gx_last=gx_last, workspace=workspace)
+    with torch.cuda.device(dev):
+        gx = torch.empty_like(x)
+        gp = torch.empty_like(x_prev) if x_prev is not None else None
+        gk, gv = torch.empty_like(mix_k), torch.empty_like(mix_v)
+        gr = torch.empty_like(mix_r) if mix_r is not None else None
+        ws = _workspace(workspace, load().wkv4_token_shift_backward_workspace(B, T, C, mix_r is not None),
+                        dev, stream)
+        rc = load().wkv4_token_shift_backward(B, T, C, _ptr(x), _ptr(x_prev), _ptr(mix_k), _ptr(mix_v),
+                                              _ptr(mix_r), _ptr(gxk), _ptr(gxv), _ptr(gxr),
+                                              _ptr(gx_last), _ptr(gx), _ptr(gp), _ptr(gk), _ptr(gv),
+                                              _ptr(gr), _ptr(ws), 0 if ws is None else ws.numel(),
+                                              _stream(stream, dev), dt)
+    if rc != 0:
+        raise Wkv4Error(rc, "wkv4_token_shift_backward")
+    return ShiftGrads(gx, gk, gv, gr, gp)
+
+
+def token_shift_backward_workspace_bytes(B: int, T: int, C: int, with_r: bool = True) -> int:
+    """wkv4_token_shift_backward_workspace: device bytes token_shift_backward needs."""
+    return int(load().wkv4_token_shift_backward_workspace(B, T, C, int(with_r)))
 
 
 def device_error(reset: bool = True) -> int:
