@@ -373,9 +373,68 @@ WKV4_API int wkv4_token_shift_backward(int64_t B, int64_t T, int64_t C, const vo
 WKV4_API size_t wkv4_token_shift_backward_workspace(int64_t B, int64_t T, int64_t C, int with_r);
 
 /*
+ * Beam search, the selection: the n best continuations of each group's K beams
+ * over a vocabulary of V tokens.  With x the logits and c the beams' scores so
+ * far (sums of log-probabilities), the candidates of group g are
+ *   s[k, v] = c[g, k] + x[g, k, v] - log sum_v' e^{x[g, k, v']},
+ * and the n largest come back in descending order, equal ones in ascending
+ * order of k V + v.
+ *   logits      [G][K] rows of V in `dtype`, row (g, k) at (g K + k) ld elements
+ *               (ld >= V: rows of a padded vocabulary).
+ *   scores      [G][K] fp32.  A beam whose score is not finite or above 2e9 in
+ *               magnitude is dead: it has no candidates.  (-INFINITY for all
+ *               beams but one starts a search.)
+ *   finished    [G][K] bytes or NULL: a beam marked non-zero goes on as it is,
+ *               with the one candidate (end_id, score unchanged); its logits
+ *               are not read.
+ *   out_scores  [G][n] fp32; out_parents, out_tokens [G][n] int32 (the beam k
+ *               and the token v of each candidate).
+ * A logit of -INFINITY is a token ruled out, a row without any other, or with
+ * a NaN or +INFINITY, has no candidates.  Where a group has fewer than n
+ * candidates the rest of its outputs are the lowest (k, v) not among them at
+ * the score -INFINITY, so parents and tokens are always valid indexes.
+ * Scores are computed in fp64 from an fp32 sum's terms and rounded once.
+ * 1 <= K <= 32, 1 <= n <= min(64, K V), K V < 2^31, G <= 2^27, 0 <= end_id < V:
+ * else WKV4_ERR_ARG.  G == 0: no-op.  Outputs must not overlap inputs or one
+ * another: WKV4_ERR_ALIAS.  One kernel, no workspace, asynchronous on `stream`.
+ */
+WKV4_API int wkv4_beam_select(int64_t G, int64_t K, int64_t V, int64_t ld, int64_t n,
+                              const void* logits, const float* scores, const uint8_t* finished,
+                              int32_t end_id, float* out_scores, int32_t* out_parents,
+                              int32_t* out_tokens, wkv4_stream_t stream, int dtype);
+
+/*
+ * Beam search, the states: after a selection beam j of group g goes on from
+ * the state of beam parents[g, j].  The states are rows of a pool of S slots
+ * (wkv4_decode_step_slots), beam j's in slot slot_ids[g, j]; the pool has P
+ * planes (3 for one layer's WKV state, 3 a layer for a whole model's, 1 for a
+ * token shift's last tokens).  The lowest beam that goes on from a parent
+ * keeps the parent's slot; its further children get copies in the slots of the
+ * group's beams that nobody goes on from, in ascending order of beam.  Only
+ * those rows are copied.
+ *   pool          [P][S][C] in `dtype`, updated in place; 16-bit types are moved
+ *                 as they are.  Rows of other slots are left as they are.
+ *   slot_ids      [G][K] int32, all distinct, each in [0, S).
+ *   parents       [G][K] int32, each in [0, K).
+ *   new_slot_ids  [G][K] int32: the slot of beam j after the call.  Depends on
+ *                 slot_ids and parents alone, so pools that share slot ids are
+ *                 moved by one call each, with the same slot_ids.
+ * A group with a slot or a parent out of range, or with one slot named twice,
+ * is left as it is (new_slot_ids = slot_ids) and sets bit 8 of the device error
+ * word; one slot named by two groups is undefined.  K <= 32, G and P <= 65535:
+ * else WKV4_ERR_ARG.  new_slot_ids must not overlap slot_ids or parents, nor
+ * the pool any of them: WKV4_ERR_ALIAS.  No allocation, asynchronous on
+ * `stream`.
+ */
+WKV4_API int wkv4_state_reorder(int64_t P, int64_t S, int64_t C, int64_t G, int64_t K, void* pool,
+                                const int32_t* slot_ids, const int32_t* parents,
+                                int32_t* new_slot_ids, wkv4_stream_t stream, int dtype);
+
+/*
  * Device-side error word of the current device (bit 1: a bounded wait for a
  * TMA copy ran out; bit 2: a bounded wait for a cluster peer's partial state
- * ran out; bit 8: a slot-indexed decode row named a slot outside its pool;
+ * ran out; bit 8: a slot-indexed decode row named a slot outside its pool, or
+ * a reordered group a bad slot or parent;
  * bit 16, bounds-checked builds only: an index outside its buffer).  One word
  * per device and process, shared by every stream and call.  Synchronises the
  * WHOLE device (cudaDeviceSynchronize: every stream, not only the caller's),

@@ -18,8 +18,8 @@ LIB = os.path.join(PKG, "libwkv4.so")
 # the bounds-checked build (WKV4_CHECKED: every global index checked, fault
 # injection switches read from the environment), for the failure tests
 CHECKED_LIB = os.path.join(PKG, "libwkv4_checked.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("wkv4_kernels.cu", "wkv4_train.cu", "wkv4_api.cpp",
-                                           "wkv4_host.cpp")]
+SOURCES = [os.path.join(CSRC, f) for f in ("wkv4_kernels.cu", "wkv4_train.cu", "wkv4_beam.cu",
+                                           "wkv4_api.cpp", "wkv4_host.cpp")]
 
 
 def deps():

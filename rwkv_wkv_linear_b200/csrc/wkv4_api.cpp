@@ -434,9 +434,51 @@ size_t wkv4_token_shift_backward_workspace(int64_t B, int64_t T, int64_t C, int 
     return wkv4::shift_backward_workspace(B, T, C, with_r ? 3 : 2);
 }
 
+int wkv4_beam_select(int64_t G, int64_t K, int64_t V, int64_t ld, int64_t n, const void* logits,
+                     const float* scores, const uint8_t* finished, int32_t end_id,
+                     float* out_scores, int32_t* out_parents, int32_t* out_tokens,
+                     wkv4_stream_t stream, int dtype) {
+    int rc = check_common(G, V, K, dtype);
+    if (rc != WKV4_OK) return rc;
+    if (G == 0) return WKV4_OK;
+    if (K < 1 || K > 32 || V < 1 || V > INT32_MAX / K || ld < V || n < 1 || n > 64 || n > K * V ||
+        G > (1ll << 27) || (finished && (end_id < 0 || end_id >= V)))
+        return WKV4_ERR_ARG;
+    const size_t es = wkv4::dtype_size(dtype);
+    if (!logits || !scores || !out_scores || !out_parents || !out_tokens || !is_aligned(logits, es))
+        return WKV4_ERR_ARG;
+    const uint64_t rows = (uint64_t)G * K, out_bytes = (uint64_t)G * n * 4;
+    const Range in[] = {range_of(logits, ((rows - 1) * ld + V) * es), range_of(scores, rows * 4),
+                        range_of(finished, rows)};
+    const Range out[] = {range_of(out_scores, out_bytes), range_of(out_parents, out_bytes),
+                         range_of(out_tokens, out_bytes)};
+    if (any_overlap(in, out)) return WKV4_ERR_ALIAS;
+    wkv4::BeamArgs a{G, K, V, ld, n, logits, scores, finished, end_id, out_scores, out_parents, out_tokens,
+                     dtype, (cudaStream_t)stream};
+    return cuda_status(wkv4::launch_beam_select(a));
+}
+
+int wkv4_state_reorder(int64_t P, int64_t S, int64_t C, int64_t G, int64_t K, void* pool,
+                       const int32_t* slot_ids, const int32_t* parents, int32_t* new_slot_ids,
+                       wkv4_stream_t stream, int dtype) {
+    int rc = check_common(P, S, C, dtype);
+    if (rc != WKV4_OK) return rc;
+    if (G < 0 || K < 0 || K > 32 || G > 65535 || P > 65535) return WKV4_ERR_ARG;
+    if (G == 0 || K == 0) return WKV4_OK;
+    if (!slot_ids || !parents || !new_slot_ids || (!pool && P * C * S > 0)) return WKV4_ERR_ARG;
+    const size_t es = wkv4::dtype_size(dtype);
+    if (!is_aligned(pool, es) || !fits_grid(1, (C * (int64_t)es + 63) / 64)) return WKV4_ERR_ARG;
+    const uint64_t rows = (uint64_t)G * K * 4;
+    const Range in[] = {range_of(slot_ids, rows), range_of(parents, rows)};
+    const Range out[] = {range_of(pool, (uint64_t)P * S * C * es), range_of(new_slot_ids, rows)};
+    if (any_overlap(in, out)) return WKV4_ERR_ALIAS;
+    wkv4::ReorderArgs a{P, S, C, G, K, pool, slot_ids, parents, new_slot_ids, dtype, (cudaStream_t)stream};
+    return cuda_status(wkv4::launch_state_reorder(a));
+}
+
 int wkv4_device_error(int reset) {
     unsigned bits = 0;
-    for (auto read : {wkv4::read_device_error, wkv4::read_train_error}) {
+    for (auto read : {wkv4::read_device_error, wkv4::read_train_error, wkv4::read_beam_error}) {
         unsigned word = 0;
         if (read(&word, reset != 0) != cudaSuccess) {
             cudaGetLastError();
@@ -457,7 +499,7 @@ const char* wkv4_status_string(int status) {
         case WKV4_ERR_CUDA: return "CUDA runtime error";
         case WKV4_ERR_TIMEOUT: return "a bounded device-side wait ran out";
         case WKV4_ERR_VARIANT: return "unknown kernel variant";
-        case WKV4_ERR_SLOT: return "a decode row named a state slot outside the pool";
+        case WKV4_ERR_SLOT: return "a state slot outside the pool, or a bad group of beams";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,79 @@
+// Launchers of the beam search kernels (wkv4_beam.cuh).
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "../../include/wkv4.h"
+#include "wkv4_beam.cuh"
+#include "wkv4_launch.cuh"
+
+namespace wkv4 {
+
+template <typename IO>
+static cudaError_t launch_beam_select_t(const BeamParams& p, int64_t G, int R, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = launch_grid(dim3((unsigned)(G * R)));
+    cfg.blockDim = dim3(kBeamThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)R;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, wkv4_beam_select_kernel<IO>, p);
+}
+
+cudaError_t launch_beam_select(const BeamArgs& a) {
+    BeamParams p{};
+    p.V = a.V;
+    p.ld = a.ld;
+    p.K = (int)a.K;
+    p.n = (int)a.n;
+    p.end_id = a.end_id;
+    p.logits = a.logits;
+    p.scores = a.scores;
+    p.finished = a.finished;
+    p.out_scores = a.out_scores;
+    p.out_parents = a.out_parents;
+    p.out_tokens = a.out_tokens;
+    // a CTA a 2048 logits of the group or more, at most 8 a cluster
+    int R = 1;
+    while (R < 8 && a.K * a.V >= 2 * R * 2048) R *= 2;
+    p.S = 1;
+    while (p.S * 2 * a.K <= R) p.S *= 2;
+    switch (a.dtype) {
+        case WKV4_F32: return launch_beam_select_t<float>(p, a.G, R, a.stream);
+        case WKV4_F16: return launch_beam_select_t<__half>(p, a.G, R, a.stream);
+        default: return launch_beam_select_t<__nv_bfloat16>(p, a.G, R, a.stream);
+    }
+}
+
+template <typename E>
+static cudaError_t launch_reorder_t(const ReorderArgs& a, int64_t row_bytes) {
+    ReorderParams p{a.P, a.S, row_bytes / (int64_t)sizeof(E), (int)a.K, a.pool, a.ids, a.parents, a.new_ids};
+    int x = 32;  // threads along a row; the rest of the block along the planes
+    while (x < 256 && x < p.row) x *= 2;
+    const int y = 256 / x;
+    // an empty pool still has new slot ids to write
+    const dim3 grid((unsigned)std::max<int64_t>(1, (p.row + x - 1) / x),
+                    (unsigned)std::max<int64_t>(1, (a.P + y - 1) / y), (unsigned)a.G);
+    return launch_pdl(wkv4_state_reorder_kernel<E>, launch_grid(grid), dim3((unsigned)x, (unsigned)y), 0,
+                      a.stream, p);
+}
+
+cudaError_t launch_state_reorder(const ReorderArgs& a) {
+    const int64_t bytes = a.C * (int64_t)dtype_size(a.dtype);
+    const uintptr_t mis = (uintptr_t)a.pool | (uintptr_t)bytes;
+    if (mis % 16 == 0) return launch_reorder_t<uint4>(a, bytes);
+    if (mis % 4 == 0) return launch_reorder_t<uint32_t>(a, bytes);
+    return launch_reorder_t<uint16_t>(a, bytes);
+}
+
+cudaError_t read_beam_error(unsigned* bits, bool reset) { return read_error_word(bits, reset); }
+
+}  // namespace wkv4

@@ -115,9 +115,37 @@ struct ShiftBwdArgs {
 cudaError_t launch_shift_backward(const ShiftBwdArgs& a);  // T, B, C >= 1
 size_t shift_backward_workspace(int64_t B, int64_t T, int64_t C, int n);
 
+// The n best continuations of each group's beams.
+struct BeamArgs {
+    int64_t G, K, V, ld, n;
+    const void* logits;
+    const float* scores;
+    const uint8_t* finished;
+    int32_t end_id;
+    float* out_scores;
+    int32_t* out_parents;
+    int32_t* out_tokens;
+    int dtype;
+    cudaStream_t stream;
+};
+cudaError_t launch_beam_select(const BeamArgs& a);  // G, K, V, n >= 1
+
+// The beams' rows of a slot pool moved to the beams that go on.
+struct ReorderArgs {
+    int64_t P, S, C, G, K;
+    void* pool;
+    const int32_t* ids;
+    const int32_t* parents;
+    int32_t* new_ids;
+    int dtype;
+    cudaStream_t stream;
+};
+cudaError_t launch_state_reorder(const ReorderArgs& a);  // G, K >= 1
+
 // Device error words of the current device, one a translation unit with
 // kernels (synchronous read; optional reset).
 cudaError_t read_device_error(unsigned* bits, bool reset);  // wkv4_kernels.cu
 cudaError_t read_train_error(unsigned* bits, bool reset);   // wkv4_train.cu
+cudaError_t read_beam_error(unsigned* bits, bool reset);    // wkv4_beam.cu
 
 }  // namespace wkv4

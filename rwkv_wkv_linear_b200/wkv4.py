@@ -26,10 +26,10 @@ STATUS = {0: "OK", -1: "ERR_ARG", -2: "ERR_DTYPE", -3: "ERR_ALIAS", -4: "ERR_CUD
 
 _DTYPES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 
-EXPORTS = ("wkv4_backward", "wkv4_backward_workspace", "wkv4_decode_step", "wkv4_decode_step_gated", "wkv4_decode_step_slots",
+EXPORTS = ("wkv4_backward", "wkv4_backward_workspace", "wkv4_beam_select", "wkv4_decode_step", "wkv4_decode_step_gated", "wkv4_decode_step_slots",
            "wkv4_device_error", "wkv4_forward", "wkv4_forward_gated", "wkv4_forward_gated_variant",
            "wkv4_forward_host", "wkv4_forward_host_workspace",
-           "wkv4_forward_variant", "wkv4_state_combine", "wkv4_status_string", "wkv4_token_shift",
+           "wkv4_forward_variant", "wkv4_state_combine", "wkv4_state_reorder", "wkv4_status_string", "wkv4_token_shift",
            "wkv4_token_shift_backward", "wkv4_token_shift_backward_workspace", "wkv4_version")
 
 _lock = threading.Lock()
@@ -86,6 +86,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             lib.wkv4_token_shift_backward.restype = i32
             lib.wkv4_token_shift_backward_workspace.argtypes = [i64, i64, i64, i32]
             lib.wkv4_token_shift_backward_workspace.restype = ctypes.c_size_t
+            lib.wkv4_beam_select.argtypes = [i64] * 5 + [vp, vp, vp, i32, vp, vp, vp, vp, i32]
+            lib.wkv4_beam_select.restype = i32
+            lib.wkv4_state_reorder.argtypes = [i64] * 5 + [vp] * 5 + [i32]
+            lib.wkv4_state_reorder.restype = i32
             lib.wkv4_device_error.argtypes = [i32]
             lib.wkv4_device_error.restype = i32
             lib.wkv4_status_string.argtypes = [i32]
@@ -581,6 +585,76 @@ def token_shift_backward(x: torch.Tensor, mix_k: torch.Tensor, mix_v: torch.Tens
 def token_shift_backward_workspace_bytes(B: int, T: int, C: int, with_r: bool = True) -> int:
     """wkv4_token_shift_backward_workspace: device bytes token_shift_backward needs."""
     return int(load().wkv4_token_shift_backward_workspace(B, T, C, int(with_r)))
+
+
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = None, *,
+                finished: Optional[torch.Tensor] = None, end_id: int = 0,
+                stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """wkv4_beam_select: logits [G, K, V] (rows of unit stride, evenly spaced: a
+    padded vocabulary may be sliced off), scores [G, K] fp32, finished [G, K]
+    bool or uint8.  Returns (scores fp32, parents int32, tokens int32), each
+    [G, n], the n best candidates of each group in descending order (n: K when
+    None)."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [G, K, V]")
+    G, K, V = logits.shape
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {logits.dtype}")
+    n = K if n is None else int(n)
+    _check_dev("scores", scores, torch.float32)
+    if finished is not None and finished.dtype not in (torch.bool, torch.uint8):
+        raise ValueError("finished must be bool or uint8")
+    _check_dev("finished", finished)
+    for name, t in (("scores", scores), ("finished", finished)):
+        if t is not None and t.shape != (G, K):
+            raise ValueError(f"{name} must be [G, K]")
+    sg, sk, sv = logits.stride()
+    ld = sk if K > 1 else sg if G > 1 else V
+    if (V > 1 and sv != 1) or ld < V or (G > 1 and K > 1 and sg != K * sk):
+        raise ValueError("logits must be rows of unit stride, evenly spaced")
+    dev = _one_device(logits=logits, scores=scores, finished=finished)
+    with torch.cuda.device(dev):
+        out = torch.empty((G, max(n, 0)), dtype=torch.float32, device=dev)
+        parents, tokens = (torch.empty((G, max(n, 0)), dtype=torch.int32, device=dev) for _ in range(2))
+        rc = load().wkv4_beam_select(G, K, V, ld, n, _ptr(logits), _ptr(scores), _ptr(finished),
+                                     int(end_id), _ptr(out), _ptr(parents), _ptr(tokens),
+                                     _stream(stream, dev), dt)
+    if rc != 0:
+        raise Wkv4Error(rc, "wkv4_beam_select")
+    return out, parents, tokens
+
+
+def state_reorder(pool: torch.Tensor, slot_ids: torch.Tensor, parents: torch.Tensor, *,
+                  new_slot_ids: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """wkv4_state_reorder: pool [P, S, C] (fp32, fp16 or bf16), updated in place
+    so that beam j of group g, whose state was in slot slot_ids[g, j], goes on
+    from the state of beam parents[g, j]; both [G, K] int32.  Returns the beams'
+    slots from then on, [G, K] int32.  Pools that share slot ids take one call
+    each, with the same slot_ids."""
+    if pool.dim() != 3:
+        raise ValueError("pool must be [P, S, C]")
+    P, S, C = pool.shape
+    dt = _DTYPES.get(pool.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {pool.dtype}")
+    if slot_ids.dim() != 2:
+        raise ValueError("slot_ids must be [G, K]")
+    _check_dev("pool", pool)
+    if new_slot_ids is None:
+        new_slot_ids = torch.empty_like(slot_ids)
+    for name, t in (("slot_ids", slot_ids), ("parents", parents), ("new_slot_ids", new_slot_ids)):
+        _check_dev(name, t, torch.int32)
+        if t.shape != slot_ids.shape:
+            raise ValueError(f"{name} must be [G, K]")
+    G, K = slot_ids.shape
+    dev = _one_device(pool=pool, slot_ids=slot_ids, parents=parents, new_slot_ids=new_slot_ids)
+    with torch.cuda.device(dev):
+        rc = load().wkv4_state_reorder(P, S, C, G, K, _ptr(pool), _ptr(slot_ids), _ptr(parents),
+                                       _ptr(new_slot_ids), _stream(stream, dev), dt)
+    if rc != 0:
+        raise Wkv4Error(rc, "wkv4_state_reorder")
+    return new_slot_ids
 
 
 def device_error(reset: bool = True) -> int:
