@@ -42,15 +42,17 @@
 // since the chunk's start), so the ascending walk accumulates the sum and the
 // chunk's end closes it.
 //
-// Numerics.  Forward states are (a, b, max) triples; (P, Q) is carried the
-// same way, P = a 2^p, Q = b 2^p with p in fp64, scaled so that the larger of
-// |a|, |b| is in [1, 2).  Within a chunk everything is held against the
-// chunk's reference 2^{max k}, under the limits of the forward's
-// fixed-reference path; (P, Q) may lie at most kFastStateLift above it.  Where
-// a limit is passed a channel takes the exact per-step path (exact_backward_*:
-// quadratic in the chunk's 16 steps, any range).  gw and gu are summed in
-// fp32: a thread's steps, then the warps, then (wkv4_column_sum_kernel) the
-// CTAs, in a fixed order.
+// Numerics.  Sums are carried as (a, b, p): A = a 2^p, D = b 2^p with an integer
+// p, so that joins scale by exact powers of two and no exponential or fp64
+// enters them; the decay over n steps is a factor in (1/2, 1] and an integer
+// exponent, worked out in fp64 once a thread.  (P, Q) is carried the same way.
+// Within a chunk everything is held against the chunk's reference 2^R,
+// R = ceil(max k log2 e), under limits like those of the forward's
+// fixed-reference path (kBwdRange, kBwdLift).  Where a limit is passed a
+// channel takes the exact per-step path (exact_backward_*: quadratic in the
+// chunk's 16 steps, fp64 exponents, any range).  gw and gu are summed in fp32:
+// a thread's steps, then the warps, then (wkv4_column_sum_kernel) the CTAs, in
+// a fixed order.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -59,12 +61,16 @@
 
 namespace wkv4 {
 
-constexpr int kBwdL = 16;   // steps a warp chunk
+// steps a warp chunk (a warp's rows are L steps x 64 channels)
+template <typename IO> constexpr int kBwdL = sizeof(IO) == 2 ? 32 : 16;
 constexpr int kBwdC = 64;   // channels a tile
+constexpr int kBwdWarps = 4;    // warps a CTA
+constexpr int kBwdMaxCtas = 8;  // CTAs a cluster
+constexpr int kBwdPitch = 68;   // sums a row of the chunks' (2 lanes a channel, 2 chunks each, meet no bank twice)
+constexpr int kSumBytes = 12;   // a sum in memory: p, a, b
 
 struct BwdParams {
     int64_t B, T, C;
-    int CGB;       // channel tiles a batch row
     int rounds;    // rounds of a cluster's steps
     const float* w;
     const float* u;
@@ -82,52 +88,153 @@ struct BwdParams {
     float* part_w;     // [rows][C] partial sums, row b NC + rank
     float* part_u;
     // rounds > 1: per round and channel the summary, then the state at the round's start
-    float* ck_a;       // [rounds][B C]
+    int* ck_p;         // [rounds][B C]
+    float* ck_a;
     float* ck_b;
-    double* ck_p;
+    uint32_t wait_rounds;  // limit of each bounded wait
     bool vec_load;     // every row starts on 16 bytes
     bool vec_store;    // channel pairs of gk, gv, gr may be stored as one access
 };
 
-// Shared memory of the backward kernel.  Per warp: k and v rows as loaded,
-// then two fp32 planes [L][64] for al and y; gout is loaded into the end of
-// the first plane and r into the end of the second, and the walk of step 3
-// overwrites them (see kRawAt).
-template <typename IO>
+// Shared memory of the backward kernel: per warp the rows of k, v, gout (and
+// r) as loaded, then the warps' chunk sums [NW], the other CTAs' sums
+// [kBwdMaxCtas] and the sum after a round [2], four barriers and the
+// tensor-memory base.
+template <typename IO, bool kGate>
 struct BwdLayout {
-    static constexpr int kRow = kBwdC * (int)sizeof(IO);
-    static constexpr int kTile = kBwdL * kRow;             // k or v rows of a warp
-    static constexpr int kPlane = kBwdL * kBwdC * 4;       // al or y of a warp
-    // The raw rows end where the plane ends.  fp32: the same bytes, row for
-    // row.  16-bit: raw row j is at kPlane/2 + 128 j, plane row i at 256 i ..
-    // 256 i + 255, which reaches raw rows j <= 2 i - 15 <= i for i < 16 only:
-    // rows already read when steps are walked upwards (a group of 4 rows is
-    // read by the whole warp before any of it is written).
-    static constexpr int kRawAt = kPlane - kTile;
-    static constexpr int kWarp = 2 * kTile + 2 * kPlane;
-    int NW;
-    __host__ __device__ size_t chunks() const { return (size_t)NW * kWarp; }
-    // chunk summaries [NW][64]: p (fp64), a, b; then the CTA's two aggregates and the start triple
-    __host__ __device__ size_t aggs() const { return chunks() + (size_t)NW * kBwdC * 16; }
-    __host__ __device__ size_t bytes() const { return aggs() + 3 * (size_t)kBwdC * 16; }
+    static constexpr int L = kBwdL<IO>;
+    static constexpr int kTile = L * kBwdC * (int)sizeof(IO);  // one tensor's rows of a warp
+    static constexpr int kWarp = (kGate ? 4 : 3) * kTile;
+    static constexpr int kChunks = kBwdWarps * kWarp;
+    static constexpr int kPeers = kChunks + kBwdWarps * kBwdPitch * kSumBytes;
+    static constexpr int kCarry = kPeers + kBwdMaxCtas * kBwdC * kSumBytes;
+    static constexpr int kBars = kCarry + 2 * kBwdC * kSumBytes;
+    static constexpr int kBytes = kBars + 5 * 8;
+    // al_t and -al_t y_t of a step's channel pair: 4 columns of tensor memory
+    static constexpr int kColumns = 4 * L;
 };
 
-// [n][64] triples in shared memory: p, then a, then b
-struct Triples {
-    double* p;
+// Limits of the fixed-reference walk: the spread of a chunk's keys in nats
+// (+ min(0, u)), so that 1 / Z <= 2^58, and how far the state before the chunk
+// or the (P, Q) behind it may lie above the reference, in powers of two.
+constexpr float kBwdRange = 40.f;
+constexpr int kBwdLift = 63;
+constexpr int kNone = -(1 << 30);  // exponent of an empty sum
+
+// A = a 2^p, D = b 2^p.
+struct Sum {
+    float a, b;
+    int p;
+};
+// 2^x = f 2^i
+struct Decay {
+    float f;
+    int i;
+};
+
+__device__ __forceinline__ Sum empty_sum() { return {0.f, 0.f, kNone}; }
+// 2^d, 0 below the normal range, d <= 127
+__device__ __forceinline__ float pow2i(int d) { return __int_as_float(max(d + 127, 0) << 23); }
+// w in log2 units as two floats.  Decays faster than 2^-32768 a step are taken
+// as that: nothing passes either, and n steps of it stay an integer exponent.
+struct Rate {
+    float hi, lo;
+};
+__device__ __forceinline__ Rate rate_of(float w) {
+    const float hi = w * kLog2e;
+    if (!(hi >= -32768.f)) return {-32768.f, 0.f};
+    constexpr float kLog2eLo = (float)(kLog2eD - (double)kLog2e);
+    return {hi, fmaf(w, kLog2e, -hi) + w * kLog2eLo};
+}
+// e^{n w}: the product split exactly into its rounded value and the rest
+__device__ __forceinline__ Decay decay_of(Rate r, int n) {
+    const float x = (float)n * r.hi;
+    const float c = ceilf(x);
+    return {ex2((x - c) + (fmaf((float)n, r.hi, -x) + (float)n * r.lo)), (int)c};
+}
+__device__ __forceinline__ Sum decayed(Sum x, Decay d) { return {x.a * d.f, x.b * d.f, x.p + d.i}; }
+// a 2^p, b 2^p with a fractional p
+__device__ __forceinline__ Sum sum_of(float a, float b, double p) {
+    const double c = ceil(fmin(fmax(p, -5e8), 5e8));
+    const float f = exp2f((float)fmax(p - c, -200.0));
+    return {a * f, b * f, (int)c};
+}
+__device__ __forceinline__ St st_of(Sum x) { return {x.a, x.b, (double)x.p}; }
+
+// x, decayed by d, and y added.
+__device__ __forceinline__ Sum join(Sum x, Sum y, Decay d) {
+    const int px = x.p + d.i, p = max(px, y.p);
+    const float fx = pow2i(px - p) * d.f, fy = pow2i(y.p - p);
+    return {fmaf(x.a, fx, y.a * fy), fmaf(x.b, fx, y.b * fy), p};
+}
+
+// x and y added.
+__device__ __forceinline__ Sum join(Sum x, Sum y) {
+    const int p = max(x.p, y.p);
+    const float fx = pow2i(x.p - p), fy = pow2i(y.p - p);
+    return {fmaf(x.a, fx, y.a * fy), fmaf(x.b, fx, y.b * fy), p};
+}
+
+// A lane's sum from another lane of the group of P that shares a channel.
+template <int P>
+__device__ __forceinline__ Sum lane_sum(Sum x, int from) {
+    return {__shfl_sync(0xffffffffu, x.a, from, P), __shfl_sync(0xffffffffu, x.b, from, P),
+            __shfl_sync(0xffffffffu, x.p, from, P)};
+}
+
+// The larger magnitude brought to [1, 2).
+__device__ __forceinline__ Sum scaled(float a, float b, int p) {
+    const float m = fmaxf(fabsf(a), fabsf(b));
+    const int e = (__float_as_int(m) >> 23) & 0xff;
+    if (m == 0.f) return empty_sum();
+    if (e == 0 || e == 255) return {a, b, p};  // subnormal, or infinite / NaN: as it is
+    const float s = __int_as_float((254 - e) << 23);
+    return {a * s, b * s, p + e - 127};
+}
+
+// [n] sums in shared memory: p, then a, then b
+struct Sums {
+    int* p;
     float* a;
     float* b;
-    __device__ __forceinline__ Triples(unsigned char* at, int n)
-        : p(reinterpret_cast<double*>(at)),
-          a(reinterpret_cast<float*>(at + (size_t)n * kBwdC * 8)),
-          b(reinterpret_cast<float*>(at + (size_t)n * kBwdC * 12)) {}
-    __device__ __forceinline__ St get(int i) const { return {a[i], b[i], p[i]}; }
-    __device__ __forceinline__ void put(int i, St s) const {
+    __device__ __forceinline__ Sums(unsigned char* at, int n)
+        : p(reinterpret_cast<int*>(at)),
+          a(reinterpret_cast<float*>(at + (size_t)n * 4)),
+          b(reinterpret_cast<float*>(at + (size_t)n * 8)) {}
+    __device__ __forceinline__ Sum get(int i) const { return {a[i], b[i], p[i]}; }
+    __device__ __forceinline__ void put(int i, Sum s) const {
         a[i] = s.a;
         b[i] = s.b;
         p[i] = s.p;
     }
+    // columns i, i + 1 (i even)
+    __device__ __forceinline__ void put2(int i, Sum s, Sum t) const {
+        *reinterpret_cast<float2*>(a + i) = make_float2(s.a, t.a);
+        *reinterpret_cast<float2*>(b + i) = make_float2(s.b, t.b);
+        *reinterpret_cast<int2*>(p + i) = make_int2(s.p, t.p);
+    }
+    __device__ __forceinline__ void get2(int i, Sum (&s)[2]) const {
+        const float2 x = *reinterpret_cast<const float2*>(a + i), y = *reinterpret_cast<const float2*>(b + i);
+        const int2 z = *reinterpret_cast<const int2*>(p + i);
+        s[0] = {x.x, y.x, z.x};
+        s[1] = {x.y, y.y, z.y};
+    }
 };
+
+// The sum written to entry i of the same array of the cluster's CTA `rank`,
+// its 12 bytes completing on that CTA's barrier `bar`.
+__device__ __forceinline__ void push_sum(const Sums& at, int i, Sum s, uint64_t* bar, int rank) {
+    const uint32_t mb = mapa_u32(smem_u32(bar), (uint32_t)rank);
+    auto put = [&](const void* p, uint32_t x) {
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                         mapa_u32(smem_u32(p), (uint32_t)rank)),
+                     "r"(x), "r"(mb)
+                     : "memory");
+    };
+    put(at.a + i, __float_as_uint(s.a));
+    put(at.b + i, __float_as_uint(s.b));
+    put(at.p + i, (uint32_t)s.p);
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -148,16 +255,16 @@ __device__ __forceinline__ void load_rows(unsigned char* dst, const IO* src, int
                                           int n, int lane, bool vec) {
     constexpr int kE = 16 / (int)sizeof(IO), kP = kBwdC / kE;  // elements a piece, pieces a row
     if (vec) {
-        const uint32_t d = smem_u32(dst);
+        constexpr int kR = 32 / kP;  // rows a pass of the warp
+        const int row = lane / kP, piece = lane % kP;
+        const int64_t c = c0 + piece * kE;
+        const int bytes = c < C ? 16 : 0;
+        const uint32_t d = smem_u32(dst) + (uint32_t)(row * kBwdC * (int)sizeof(IO) + piece * 16);
+        const IO* s = src + (int64_t)row * C + (c < C ? c : 0);
 #pragma unroll
-        for (int q = 0; q < kBwdL * kP / 32; ++q) {
-            const int row = (q * 32 + lane) / kP, piece = (q * 32 + lane) % kP;
-            const int64_t c = c0 + piece * kE;
-            if (row < n) {
-                const bool in = c < C;
-                cp_async16(d + (uint32_t)(row * kBwdC * (int)sizeof(IO) + piece * 16),
-                           src + (int64_t)row * C + (in ? c : 0), in ? 16 : 0);
-            }
+        for (int q = 0; q < kBwdL<IO> / kR; ++q) {
+            if (q * kR + row < n) cp_async16(d + (uint32_t)(q * kR * kBwdC * (int)sizeof(IO)), s, bytes);
+            s += (int64_t)kR * C;
         }
     } else {
         IO* d = reinterpret_cast<IO*>(dst);
@@ -171,14 +278,10 @@ __device__ __forceinline__ void load_rows(unsigned char* dst, const IO* src, int
     }
 }
 
-// (P, Q) with a common exponent: the larger magnitude brought to [1, 2).
-__device__ __forceinline__ St scaled(float P, float Q, double p) {
-    const float m = fmaxf(fabsf(P), fabsf(Q));
-    const int e = ((__float_as_int(m) >> 23) & 0xff);
-    if (m == 0.f) return empty_state();
-    if (e == 0 || e == 255) return {P, Q, p};  // subnormal, or infinite / NaN: as it is
-    const float s = __int_as_float((254 - e) << 23);
-    return {P * s, Q * s, p + (double)(e - 127)};
+// The same with an fp64 exponent, for the exact paths.
+__device__ __forceinline__ St scaled_st(float P, float Q, double p) {
+    const Sum x = scaled(P, Q, 0);
+    return x.p == kNone ? empty_state() : St{x.a, x.b, p + (double)x.p};
 }
 
 // Gradients through the gate: g = s gout and, through the pointer, gr.
@@ -231,10 +334,10 @@ __device__ __noinline__ St exact_backward_up(const ExactChunk<IO> c, IO* gr_out)
             gr_out[o] = Io<IO>::from_f(gr);
         }
         const float al = g * e.rz;
-        acc = combine(acc, scaled(al, -al * e.y, (double)i * c.w2 - e.q), 0.0);
+        acc = combine(acc, scaled_st(al, -al * e.y, (double)i * c.w2 - e.q), 0.0);
         exact_update(s, k, v, c.w2);
     }
-    return scaled(acc.a, acc.b, acc.p);
+    return scaled_st(acc.a, acc.b, acc.p);
 }
 
 struct ExactGrads {
@@ -272,16 +375,14 @@ __device__ __noinline__ ExactGrads exact_backward_down(const ExactChunk<IO> c, S
         gu += gut;
         gw += (float)(exp2(fmin(R.p + s.p + c.w2, 1000.0)) *
                       ((double)R.a * s.a + (double)R.b * s.b));
-        R = combine(R, scaled(al, -al * e.y, -e.q), c.w2);
-        R = scaled(R.a, R.b, R.p);
+        R = combine(R, scaled_st(al, -al * e.y, -e.q), c.w2);
+        R = scaled_st(R.a, R.b, R.p);
     }
     return {R, gw, gu};
 }
 
 // Steps of a chunk starting at t.
-__device__ __forceinline__ int chunk_steps(int64_t T, int64_t t, int most) {
-    return (int)max((int64_t)0, min((int64_t)most, T - t));
-}
+__device__ __forceinline__ int chunk_steps(int T, int t, int most) { return max(0, min(most, T - t)); }
 
 // One pair's stores of a gradient row.
 template <typename IO>
@@ -294,379 +395,612 @@ __device__ __forceinline__ void store_pair(IO* p, f2 x, bool vec, bool ok0, bool
     }
 }
 
+constexpr f2 kSigns = 0x8000000080000000ull;
+
+// A pair's decay and bonus.
+struct BwdConsts {
+    f2 ew, eu;
+    float w[2], u[2];
+    __device__ __forceinline__ BwdConsts(const float* gw, const float* gu, int64_t c, int64_t C) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            w[j] = c + j < C ? __ldg(gw + c + j) : 0.f;
+            u[j] = c + j < C ? __ldg(gu + c + j) : 0.f;
+        }
+        ew = pk(expf(w[0]), expf(w[1]));
+        eu = pk(expf(u[0]), expf(u[1]));
+    }
+};
+
+// A pair's chunk reference (a whole power of two at or above its largest key)
+// and whether each channel may be held against it.
+struct BwdRef {
+    float R[2];
+    bool fast[2];
+};
+
+// The chunk's sums from the empty state.
+template <typename IO, bool kFull>
+__device__ __forceinline__ void bwd_summary(const IO* sk, const IO* sv, int col, int n,
+                                            const BwdConsts& cc, BwdRef& ref, Sum (&sum)[2]) {
+    constexpr int L = kBwdL<IO>;
+    typename Pair<IO>::Raw mx = Pair<IO>::raw(sk + col), mn = mx;
+#pragma unroll
+    for (int i = 1; i < L; ++i)
+        if (kFull || i < n) Pair<IO>::minmax(Pair<IO>::raw(sk + i * kBwdC + col), mx, mn);
+    float kmax[2], kmin[2];
+    Pair<IO>::bounds(mx, mn, kmax, kmin);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float R = ceilf(kmax[j] * kLog2e);
+        ref.fast[j] = kmax[j] - kmin[j] <= kBwdRange + fminf(0.f, cc.u[j]) && cc.u[j] <= kFastMaxU &&
+                      cc.w[j] <= kFastMaxW && fabsf(R) <= 4194304.f;
+        ref.R[j] = fabsf(R) <= 4194304.f ? R : 0.f;
+    }
+    const f2 l2e = pk(kLog2e, kLog2e), nref = pk(-ref.R[0], -ref.R[1]);
+    f2 A = 0ull, D = 0ull;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if (kFull || i < n) {
+            const f2 e = ex2_2(fma2(Pair<IO>::load(sk + i * kBwdC + col), l2e, nref));
+            A = fma2(e, Pair<IO>::load(sv + i * kBwdC + col), mul2(cc.ew, A));
+            D = fma2(cc.ew, D, e);
+        }
+    }
+    const float Aj[2] = {lo(A), hi(A)}, Dj[2] = {lo(D), hi(D)};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (ref.fast[j]) {  // D is a normal positive number: bring it to [1, 2)
+            const int e = (__float_as_int(Dj[j]) >> 23) & 0xff;
+            const float s = __int_as_float((254 - e) << 23);
+            sum[j] = {Aj[j] * s, Dj[j] * s, (int)ref.R[j] + e - 127};
+        } else {
+            const St x = slow_summary<IO>(sk + col + j, sv + col + j, kBwdC, n, (double)cc.w[j] * kLog2eD);
+            sum[j] = sum_of(x.a, x.b, x.p);
+        }
+    }
+}
+
+template <typename IO>
+__device__ __forceinline__ void bwd_summary_n(const IO* sk, const IO* sv, int col, int n,
+                                              const BwdConsts& cc, BwdRef& ref, Sum (&sum)[2]) {
+    if (n >= kBwdL<IO>) {
+        bwd_summary<IO, true>(sk, sv, col, n, cc, ref, sum);
+    } else if (n > 0) {
+        bwd_summary<IO, false>(sk, sv, col, n, cc, ref, sum);
+    } else {
+        sum[0] = sum[1] = empty_sum();
+        ref.fast[0] = ref.fast[1] = false;
+        ref.R[0] = ref.R[1] = 0.f;
+    }
+}
+
+// One warp's chunk in shared memory.
+template <typename IO>
+struct BwdChunk {
+    const IO* k;
+    const IO* v;
+    const IO* gy;
+    const IO* r;
+    uint32_t stash;  // tensor memory: al_t, -al_t y_t of the lane's pair, 4 columns a step
+    int col, n;
+};
+
+// Warp-wide: 32 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+    // the wait is tied to the registers, so no use of them is scheduled before it
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// What the upward walk leaves: shares of gw, gu, the derivatives of A, D by w,
+// and (P, Q) of the chunk alone times 2^kUpShift.
+struct BwdUp {
+    f2 gw, gu, Ap, Dp, P, Q;
+};
+// The weight e^{iw} of step i in the chunk's (P, Q) starts at 2^40, so that
+// under a fast decay it stays a float as long as al (up to 2^58 g) can make up
+// for it; 2^98 times a gradient of 2^29 is still in range.
+constexpr int kUpShift = 40;
+
+// Step 3.  kPlain: a whole chunk, every lane's two channels on the
+// fixed-reference path, rows stored as pairs.
+template <typename IO, bool kGate, bool kPlain>
+__device__ __forceinline__ void bwd_walk_up(const BwdChunk<IO>& ch, const BwdConsts& cc, f2 nref, f2 A,
+                                            f2 D, IO* gr, int64_t C, bool vec, bool s0, bool s1, BwdUp& o) {
+    const f2 l2e = pk(kLog2e, kLog2e), one = pk(1.f, 1.f), m1 = pk(-1.f, -1.f);
+    f2 Ap = 0ull, Dp = 0ull, gw = 0ull, gu = 0ull, P = 0ull, Q = 0ull;
+    f2 f = pk(0x1p40f, 0x1p40f);
+#pragma unroll(kPlain ? 2 : 1)
+    for (int q = 0; q < (kPlain ? kBwdL<IO> : ch.n); q += 4) {
+        uint32_t st[16];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int i = q + s;
+            if (kPlain || i < ch.n) {
+                const f2 e = ex2_2(fma2(Pair<IO>::load(ch.k + i * kBwdC + ch.col), l2e, nref));
+                const f2 v = Pair<IO>::load(ch.v + i * kBwdC + ch.col);
+                const f2 ee = mul2(cc.eu, e);
+                const f2 rz = rcp2(add2(D, ee));
+                const f2 ny = mul2(mul2(fma2(ee, v, A), m1), rz);
+                f2 g = Pair<IO>::load(ch.gy + i * kBwdC + ch.col);
+                if constexpr (kGate) {
+                    const f2 x0 = mul2(Pair<IO>::load(ch.r + i * kBwdC + ch.col), pk(-kLog2e, -kLog2e));
+                    // (above 2^126 the gate is 0 to within its rounding, and x s stays finite)
+                    const f2 x = pk(ex2(fminf(lo(x0), 126.f)), ex2(fminf(hi(x0), 126.f)));
+                    const f2 sg = rcp2(add2(one, x));
+                    g = mul2(g, sg);
+                    const f2 grv = mul2(mul2(g, ny), mul2(x, sg)) ^ kSigns;
+                    if constexpr (kPlain)
+                        Pair<IO>::store(gr, grv);
+                    else
+                        store_pair(gr, grv, vec, s0, s1);
+                    gr += C;
+                }
+                const f2 al = mul2(g, rz);
+                const f2 nay = mul2(al, ny);
+                st[4 * s] = (uint32_t)al;
+                st[4 * s + 1] = (uint32_t)(al >> 32);
+                st[4 * s + 2] = (uint32_t)nay;
+                st[4 * s + 3] = (uint32_t)(nay >> 32);
+                gu = fma2(mul2(ee, al), add2(v, ny), gu);
+                gw = fma2(al, Ap, fma2(nay, Dp, gw));
+                P = fma2(f, al, P);
+                Q = fma2(f, nay, Q);
+                f = mul2(f, cc.ew);
+                const f2 t1 = mul2(cc.ew, A), t2 = mul2(cc.ew, D);
+                Ap = fma2(cc.ew, Ap, t1);
+                Dp = fma2(cc.ew, Dp, t2);
+                A = fma2(e, v, t1);
+                D = add2(t2, e);
+            } else {
+                st[4 * s] = st[4 * s + 1] = st[4 * s + 2] = st[4 * s + 3] = 0;
+            }
+        }
+        __syncwarp();  // tensor-memory accesses are warp-collective
+        tmem_st16(ch.stash + 4 * q, st);
+    }
+    tmem_wait_st();
+    o = {gw, gu, Ap, Dp, P, Q};
+}
+
+// Step 5: gk, gv from (P, Q) at the chunk's end; (P, Q) at its start in P, Q.
+// With h = e^u al + P and j = -e^u al y + Q: gv = e h, gk = e (h v + j).
+template <typename IO, bool kPlain>
+__device__ __forceinline__ void bwd_walk_down(const BwdChunk<IO>& ch, const BwdConsts& cc, f2 nref, f2& P,
+                                              f2& Q, IO* gk, IO* gv, int64_t C, bool vec, bool s0, bool s1) {
+    const f2 l2e = pk(kLog2e, kLog2e);
+    const int n = kPlain ? kBwdL<IO> : ch.n;
+    gk += (int64_t)(n - 1) * C;
+    gv += (int64_t)(n - 1) * C;
+#pragma unroll 1
+    for (int q = (n - 1) & ~7; q >= 0; q -= 8) {
+        uint32_t st[32];
+        __syncwarp();
+        tmem_ld32(ch.stash + 4 * q, st);
+#pragma unroll
+        for (int s = 7; s >= 0; --s) {
+            const int i = q + s;
+            if (kPlain || i < n) {
+                const f2 e = ex2_2(fma2(Pair<IO>::load(ch.k + i * kBwdC + ch.col), l2e, nref));
+                const f2 v = Pair<IO>::load(ch.v + i * kBwdC + ch.col);
+                const f2 al = pku(st[4 * s], st[4 * s + 1]), nay = pku(st[4 * s + 2], st[4 * s + 3]);
+                const f2 h = fma2(cc.eu, al, P), j = fma2(cc.eu, nay, Q);
+                const f2 xv = mul2(e, h), xk = mul2(e, fma2(h, v, j));
+                if constexpr (kPlain) {
+                    Pair<IO>::store(gv, xv);
+                    Pair<IO>::store(gk, xk);
+                } else {
+                    store_pair(gv, xv, vec, s0, s1);
+                    store_pair(gk, xk, vec, s0, s1);
+                }
+                gv -= C;
+                gk -= C;
+                P = fma2(cc.ew, P, al);
+                Q = fma2(cc.ew, Q, nay);
+            }
+        }
+    }
+}
+
 template <typename IO, bool kGate>
-__global__ void __launch_bounds__(256, 2) wkv4_backward_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const BwdParams p) {
     namespace cg = cooperative_groups;
     allow_dependents();
     grid_dependency_wait();
-    using Lay = BwdLayout<IO>;
-    constexpr int L = kBwdL;
+    using Lay = BwdLayout<IO, kGate>;
+    constexpr int NW = kBwdWarps, L = kBwdL<IO>, Ts = NW * L;  // steps of a chunk, of a CTA in a round
+    constexpr int P = NW / 2;              // threads that join a channel's chunks, two chunks each
+    constexpr unsigned kAll = 0xffffffffu;
     extern __shared__ __align__(16) unsigned char smem[];
-    const int NW = blockDim.x >> 5;
     cg::cluster_group cluster = cg::this_cluster();
     const int NC = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const Lay lay{NW};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 2 * lane;
-    const int64_t tile = blockIdx.x / NC;
-    const int64_t b = tile / p.CGB, c0 = (tile - b * p.CGB) * kBwdC;
-    const int64_t T = p.T, C = p.C, BC = p.B * C;
-    const int Ts = NW * L;                    // steps of this CTA in a round
-    const int64_t round_steps = (int64_t)NC * Ts;
+    const int b = blockIdx.y, c0 = (int)(blockIdx.x >> (__ffs(NC) - 1)) * kBwdC;
+    const int T = (int)p.T;
+    const int64_t C = p.C, BC = p.B * C;
+    const int round_steps = NC * Ts;
     const int64_t c = c0 + col;
     const bool ok0 = c < C, ok1 = c + 1 < C;
-
-    unsigned char* const wbase = smem + (size_t)warp * Lay::kWarp;
-    const IO* const sk = reinterpret_cast<const IO*>(wbase);
-    const IO* const sv = reinterpret_cast<const IO*>(wbase + Lay::kTile);
-    unsigned char* const plane1 = wbase + 2 * Lay::kTile;
-    unsigned char* const plane2 = plane1 + Lay::kPlane;
-    const IO* const sg = reinterpret_cast<const IO*>(plane1 + Lay::kRawAt);
-    const IO* const sr = reinterpret_cast<const IO*>(plane2 + Lay::kRawAt);
-    float* const sal = reinterpret_cast<float*>(plane1);
-    float* const sy = reinterpret_cast<float*>(plane2);
-    const Triples chunk(smem + lay.chunks(), NW);
-    const Triples aggF(smem + lay.aggs(), 1), aggR(smem + lay.aggs() + kBwdC * 16, 1),
-        start(smem + lay.aggs() + 2 * kBwdC * 16, 1);
-
     // every global access below is (b T + t) C + c for t < T, c < C, or b C + c
     if (!in_range(b, p.B)) return;
-    PairConsts cc;
-    pair_consts(p.w, p.u, c, C, cc);
+    const int64_t row0 = (int64_t)b * T;
 
-    // the 64 threads that join chunks and CTAs: a channel each
-    const int jc = threadIdx.x;
-    const bool joiner = jc < kBwdC;
-    const bool jok = joiner && c0 + jc < C;
-    const int64_t jch = b * C + c0 + jc;
-    const double jw2 = jok ? (double)p.w[c0 + jc] * kLog2eD : 0.0;
-    St Rcarry = empty_state();  // (P, Q) after the current round's last step
-    if (jok && p.gstate_out)
-        Rcarry = scaled(p.gstate_out[jch], p.gstate_out[BC + jch],
-                        -(double)p.state_out[2 * BC + jch] * kLog2eD);
+    unsigned char* const wbase = smem + warp * Lay::kWarp;
+    const Sums chunk(smem + Lay::kChunks, NW * kBwdPitch);
+    const Sums peers(smem + Lay::kPeers, kBwdMaxCtas * kBwdC);  // row q: CTA q's sum (below rank forward, above backward)
+    const Sums after(smem + Lay::kCarry, 2 * kBwdC);            // (P, Q) after a round, by the round's parity
+    // barriers: the lower ranks' forward sums, the higher ranks' (P, Q), the two rows of `after`
+    uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + Lay::kBars);
+    uint32_t* const tslot = reinterpret_cast<uint32_t*>(bar + 4);
 
-    f2 gw_sum = 0ull, gu_sum = 0ull;
-    const f2 l2e = pk(kLog2e, kLog2e);
-
-    for (int round = p.rounds - 1; round >= 0; --round) {
-        const int64_t t_round = (int64_t)round * round_steps;
-        const int64_t t_cta = t_round + (int64_t)rank * Ts;
-        const int64_t t0 = t_cta + warp * L;
+    auto load_chunk = [&](int round) {
+        const int t0 = round * round_steps + rank * Ts + warp * L;
         const int n = chunk_steps(T, t0, L);
-        const int64_t at = (b * T + t0) * C;  // element offset of the chunk's first row
         if (n > 0) {
+            const int64_t at = (row0 + t0) * C;
             load_rows<IO>(wbase, static_cast<const IO*>(p.k) + at, C, c0, n, lane, p.vec_load);
             load_rows<IO>(wbase + Lay::kTile, static_cast<const IO*>(p.v) + at, C, c0, n, lane,
                           p.vec_load);
             cp_async_commit();
-            load_rows<IO>(plane1 + Lay::kRawAt, static_cast<const IO*>(p.gy) + at, C, c0, n, lane,
+            load_rows<IO>(wbase + 2 * Lay::kTile, static_cast<const IO*>(p.gy) + at, C, c0, n, lane,
                           p.vec_load);
             if constexpr (kGate)
-                load_rows<IO>(plane2 + Lay::kRawAt, static_cast<const IO*>(p.r) + at, C, c0, n,
+                load_rows<IO>(wbase + 3 * Lay::kTile, static_cast<const IO*>(p.r) + at, C, c0, n,
                               lane, p.vec_load);
         } else {
             cp_async_commit();
         }
         cp_async_commit();
+    };
+    load_chunk(p.rounds - 1);
+    if (threadIdx.x < 4) mbar_init(bar + threadIdx.x, 1);
+    if (threadIdx.x == 0) fence_mbar_init();
+    if (warp == 0) tmem_alloc(tslot, Lay::kColumns);
+    tmem_fence_before_sync();
+    cluster.sync();  // every CTA's barriers are set up before a peer's sum may arrive
+    tmem_fence_after_sync();
+    // the lane quarter of tensor memory that this warp reaches
+    const uint32_t taddr = *tslot + ((uint32_t)warp << 21);
+    BwdChunk<IO> ch{reinterpret_cast<const IO*>(wbase), reinterpret_cast<const IO*>(wbase + Lay::kTile),
+                    reinterpret_cast<const IO*>(wbase + 2 * Lay::kTile),
+                    reinterpret_cast<const IO*>(wbase + (kGate ? 3 : 2) * Lay::kTile), taddr, col, 0};
+
+    const BwdConsts cc(p.w, p.u, c, C);
+    // this thread's part in the joins: chunks 2 part, 2 part + 1 of channel jc,
+    // and CTAs q0 .. q0 + qn - 1 of the cluster
+    const int jc = threadIdx.x / P, part = threadIdx.x % P;
+    const bool jok = c0 + jc < C;
+    const int64_t jch = (int64_t)b * C + c0 + jc;
+    const Rate rate = rate_of(jok ? p.w[c0 + jc] : 0.f);
+    const Decay dL = decay_of(rate, L), d2 = decay_of(rate, 2 * L), d4 = decay_of(rate, 4 * L),
+                dT = decay_of(rate, Ts);
+    const Decay d_before = decay_of(rate, 2 * part * L), d_after = decay_of(rate, (NW - 2 - 2 * part) * L);
+    const int qn = max(1, NC / P), q0 = min(part * qn, NC), q1 = min(q0 + qn, NC);
+    // from the end of CTA min(q1, rank) - 1 to this CTA's start; from the start
+    // of CTA max(q0, rank + 1) to this CTA's end
+    const Decay d_up = decay_of(rate, (rank - min(q1, rank)) * Ts);
+    const Decay d_down = decay_of(rate, (max(q0, rank + 1) - (rank + 1)) * Ts);
+    const int last = p.rounds - 1;
+    // (P, Q) after the last step, carried on to the end of the last round (as if
+    // the recurrence ran on there): every chunk is then a whole one to the joins
+    Sum Rlast = empty_sum();
+    if (jok && p.gstate_out) {
+        const Sum x = sum_of(p.gstate_out[jch], p.gstate_out[BC + jch],
+                             -(double)p.state_out[2 * BC + jch] * kLog2eD);
+        const int pad = (last + 1) * round_steps - T;
+        const Decay d = decay_of(Rate{-rate.hi, -rate.lo}, pad);
+        Rlast = scaled(x.a * d.f, x.b * d.f, x.p + d.i);
+    }
+    bool failed = false;  // a bounded wait ran out: go on without waiting (the results are reported bad)
+    auto wait = [&](int which, uint32_t parity) {
+        if (failed || mbar_wait_cluster_bounded(bar + which, parity, p.wait_rounds)) return;
+        atomicOr(&g_device_error, kErrExchangeWait);
+        failed = true;
+    };
+
+    f2 gw_sum = 0ull, gu_sum = 0ull;
+
+    for (int round = last; round >= 0; --round) {
+        const int it = last - round;
+        const uint32_t parity = it & 1;
+        const int t0 = round * round_steps + rank * Ts + warp * L;
+        const int n = ch.n = chunk_steps(T, t0, L);
+        const int64_t at = (row0 + t0) * C;  // element offset of the chunk's first row
+        if (it > 0) load_chunk(round);
+        if (threadIdx.x == 0) {  // what this round's barriers will receive
+            if (rank > 0) mbar_arrive_expect_tx(bar, (uint32_t)rank * kBwdC * kSumBytes);
+            if (rank < NC - 1) mbar_arrive_expect_tx(bar + 1, (uint32_t)(NC - 1 - rank) * kBwdC * kSumBytes);
+            if (rank > 0 && it > 0) mbar_arrive_expect_tx(bar + 2 + parity, kBwdC * kSumBytes);
+        }
         // the state at the round's start
-        St carry = empty_state();
-        if (jok) {
+        Sum carry = empty_sum();
+        if (jok && part == 0) {
             if (p.rounds > 1) {
                 const int64_t i = (int64_t)round * BC + jch;
                 carry = {p.ck_a[i], p.ck_b[i], p.ck_p[i]};
             } else if (p.state_in) {
-                carry = load_state_log2(p.state_in, BC, jch);
+                carry = sum_of(p.state_in[jch], p.state_in[BC + jch],
+                               (double)p.state_in[2 * BC + jch] * kLog2eD);
             }
         }
         cp_async_wait<1>();
         __syncwarp();
 
         // 1. the chunk's summary
-        PairRef ref;
-        St sum[2];
-        chunk_phase1<IO, L>(ref, sk, sv, kBwdC, col, n, cc, sum);
-        __syncthreads();  // the last round's suffixes have been read
-        chunk.put(warp * kBwdC + col, sum[0]);
-        chunk.put(warp * kBwdC + col + 1, sum[1]);
-        __syncthreads();
-
-        // 2. prefixes within the CTA, then over the cluster
-        if (joiner) {
-            St acc = empty_state();
-            for (int q = 0; q < NW; ++q) {
-                const St x = chunk.get(q * kBwdC + jc);
-                chunk.put(q * kBwdC + jc, acc);
-                acc = combine(acc, x, (double)chunk_steps(T, t_cta + q * L, L) * jw2);
-            }
-            aggF.put(jc, acc);
-        }
-        cluster.sync();
-        if (joiner) {
-            for (int q = 0; q < rank; ++q) {
-                const St x{*cluster.map_shared_rank(aggF.a + jc, q),
-                           *cluster.map_shared_rank(aggF.b + jc, q),
-                           *cluster.map_shared_rank(aggF.p + jc, q)};
-                carry = combine(carry, x, (double)chunk_steps(T, t_round + (int64_t)q * Ts, Ts) * jw2);
-            }
-            start.put(jc, carry);
+        BwdRef ref;
+        {
+            Sum sum[2];
+            bwd_summary_n<IO>(ch.k, ch.v, col, n, cc, ref, sum);
+            chunk.put2(warp * kBwdPitch + col, sum[0], sum[1]);
         }
         __syncthreads();
 
-        // 3. the chunk from the state at its start: y, al, gr, and (P, Q) of the chunk alone
-        St S[2];
+        // 2. the state at every chunk's start: a scan over the CTA's chunks, the
+        // lower ranks' sums, and the state at the round's start
+        {
+            const int i0 = 2 * part * kBwdPitch + jc, i1 = i0 + kBwdPitch;
+            const Sum x0 = chunk.get(i0);
+            Sum y = join(x0, chunk.get(i1), dL);
+            Sum o = lane_sum<P>(y, part - 1);
+            if (part >= 1) y = join(o, y, d2);
+            if constexpr (P == 4) {
+                o = lane_sum<P>(y, part - 2);
+                if (part >= 2) y = join(o, y, d4);
+            }
+            const Sum total = lane_sum<P>(y, P - 1);
+            Sum ex = lane_sum<P>(y, part - 1);
+            if (part == 0) ex = empty_sum();
+            for (int q = rank + 1 + part; q < NC; q += P) push_sum(peers, rank * kBwdC + jc, total, bar, q);
+            Sum s = carry;  // part 0: the round's start; the others: empty
+            if (rank > 0) {
+                wait(0, parity);
+                for (int q = q0; q < min(q1, rank); ++q) s = join(s, peers.get(q * kBwdC + jc), dT);
+                s = decayed(s, d_up);
+#pragma unroll
+                for (int h = 1; h < P; h *= 2) s = join(s, lane_sum<P>(s, part ^ h));
+            } else {
+                s = lane_sum<P>(s, 0);
+            }
+            const Sum S0 = join(s, ex, d_before);
+            chunk.put(i0, S0);
+            chunk.put(i1, join(S0, x0, dL));
+        }
+        __syncthreads();
+
+        // 3. the chunk from the state at its start
+        Sum S[2];
+        chunk.get2(warp * kBwdPitch + col, S);
         bool fast[2];
         float a0[2], b0[2];
-        const double before = (double)(chunk_steps(T, t_cta, warp * L));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            S[j] = combine(start.get(col + j), chunk.get(warp * kBwdC + col + j), before * cc.w2[j]);
-            const double lift = S[j].p - (double)ref.kref[j];
-            fast[j] = ref.fast[j] && lift <= (double)(kFastStateLift * kLog2e);
-            const float sc = ex2((float)lift);
+            const int lift = S[j].p - (int)ref.R[j];
+            fast[j] = ref.fast[j] && lift <= kBwdLift;
+            const float sc = pow2i(min(lift, 127));
             a0[j] = S[j].a * sc;
             b0[j] = S[j].b * sc;
         }
         cp_async_wait<0>();
         __syncwarp();
-        const f2 nref = pk(-ref.kref[0], -ref.kref[1]);
-        f2 A = pk(a0[0], a0[1]), D = pk(b0[0], b0[1]);
-        f2 Ap = 0ull, Dp = 0ull;  // derivatives by w since the chunk's start
-        f2 gw = 0ull, gu = 0ull;
+        const f2 nref = pk(-ref.R[0], -ref.R[1]);
         IO* const gr = kGate ? static_cast<IO*>(p.gr) + at + c : nullptr;
-#pragma unroll 1
-        for (int q = 0; q < n; q += 4) {
-            f2 gg[4], rr[4];
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                gg[s] = Pair<IO>::load(sg + (q + s) * kBwdC + col);
-                if constexpr (kGate) rr[s] = Pair<IO>::load(sr + (q + s) * kBwdC + col);
-            }
-            __syncwarp();  // the rows this group overwrites have been read by every lane
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int i = q + s;
-                if (i < n) {
-                    const f2 e = ex2_2(fma2(Pair<IO>::load(sk + i * kBwdC + col), l2e, nref));
-                    const f2 v = Pair<IO>::load(sv + i * kBwdC + col);
-                    const f2 ee = mul2(cc.eu, e);
-                    const f2 rz = rcp2(add2(D, ee));
-                    const f2 y = mul2(fma2(ee, v, A), rz);
-                    const f2 ny = y ^ 0x8000000080000000ull;
-                    f2 g = gg[s];
-                    if constexpr (kGate) {
-                        const f2 x0 = mul2(rr[s], pk(-kLog2e, -kLog2e));
-                        const f2 x = pk(ex2(fminf(lo(x0), 126.f)), ex2(fminf(hi(x0), 126.f)));
-                        const f2 sgm = rcp2(add2(pk(1.f, 1.f), x));
-                        g = mul2(g, sgm);
-                        store_pair(gr + (int64_t)i * C, mul2(mul2(g, y), mul2(x, sgm)), p.vec_store,
-                                   ok0 && fast[0], ok1 && fast[1]);
-                    }
-                    const f2 al = mul2(g, rz);
-                    *reinterpret_cast<f2*>(sal + i * kBwdC + col) = al;
-                    *reinterpret_cast<f2*>(sy + i * kBwdC + col) = y;
-                    gu = fma2(mul2(ee, al), add2(v, ny), gu);
-                    gw = fma2(al, fma2(ny, Dp, Ap), gw);
-                    const f2 t1 = mul2(cc.ew, A), t2 = mul2(cc.ew, D);
-                    Ap = fma2(cc.ew, Ap, t1);
-                    Dp = fma2(cc.ew, Dp, t2);
-                    A = fma2(e, v, t1);
-                    D = add2(t2, e);
-                }
-            }
-        }
-        f2 P = 0ull, Q = 0ull;
-#pragma unroll 4
-        for (int i = n - 1; i >= 0; --i) {
-            const f2 al = *reinterpret_cast<const f2*>(sal + i * kBwdC + col);
-            const f2 y = *reinterpret_cast<const f2*>(sy + i * kBwdC + col);
-            P = fma2(cc.ew, P, al);
-            Q = fma2(cc.ew, Q, mul2(al, y ^ 0x8000000080000000ull));
-        }
-        St loc[2];
-        const float Pj[2] = {lo(P), hi(P)}, Qj[2] = {lo(Q), hi(Q)};
+        BwdUp up;
+        const bool plain = __all_sync(kAll, n == L && p.vec_store && ok1 && fast[0] && fast[1]);
+        if (plain)
+            bwd_walk_up<IO, kGate, true>(ch, cc, nref, pk(a0[0], a0[1]), pk(b0[0], b0[1]), gr, C, true, true,
+                                         true, up);
+        else
+            bwd_walk_up<IO, kGate, false>(ch, cc, nref, pk(a0[0], a0[1]), pk(b0[0], b0[1]), gr, C,
+                                          p.vec_store, ok0 && fast[0], ok1 && fast[1], up);
         auto exact_chunk = [&](int j) {
             return ExactChunk<IO>{static_cast<const IO*>(p.k) + at + c + j,
                                   static_cast<const IO*>(p.v) + at + c + j,
                                   static_cast<const IO*>(p.gy) + at + c + j,
                                   kGate ? static_cast<const IO*>(p.r) + at + c + j : nullptr,
-                                  C, n, cc.w2[j], (double)cc.u[j] * kLog2eD, S[j]};
+                                  C, n, (double)cc.w[j] * kLog2eD, (double)cc.u[j] * kLog2eD, st_of(S[j])};
         };
+        {
+            Sum loc[2];
+            const float Pj[2] = {lo(up.P), hi(up.P)}, Qj[2] = {lo(up.Q), hi(up.Q)};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if (n == 0 || !(j ? ok1 : ok0)) {
-                loc[j] = empty_state();
-            } else if (fast[j]) {
-                loc[j] = scaled(Pj[j], Qj[j], -(double)ref.kref[j]);
-            } else {
-                loc[j] = exact_backward_up<IO>(exact_chunk(j), gr + j);
+            for (int j = 0; j < 2; ++j) {
+                if (n == 0 || !(j ? ok1 : ok0)) {
+                    loc[j] = empty_sum();
+                } else if (fast[j]) {
+                    loc[j] = scaled(Pj[j], Qj[j], -(int)ref.R[j] - kUpShift);
+                } else {
+                    const St x = exact_backward_up<IO>(exact_chunk(j), gr + j);
+                    const Sum y = sum_of(x.a, x.b, x.p);
+                    loc[j] = scaled(y.a, y.b, y.p);
+                }
             }
-        }
-        __syncthreads();  // the prefixes have been read
-        chunk.put(warp * kBwdC + col, loc[0]);
-        chunk.put(warp * kBwdC + col + 1, loc[1]);
-        __syncthreads();
-
-        // 4. suffixes within the CTA, then over the cluster
-        if (joiner) {
-            St acc = empty_state();
-            for (int q = NW - 1; q >= 0; --q) {
-                const St x = chunk.get(q * kBwdC + jc);
-                chunk.put(q * kBwdC + jc, acc);
-                // what comes after the chunk reaches its start through the chunk's own decay
-                acc = combine(acc, x, (double)chunk_steps(T, t_cta + q * L, L) * jw2);
-            }
-            aggR.put(jc, acc);
-        }
-        cluster.sync();
-        if (joiner) {
-            for (int q = NC - 1; q >= 0; --q) {
-                if (q == rank) start.put(jc, Rcarry);
-                const St x{*cluster.map_shared_rank(aggR.a + jc, q),
-                           *cluster.map_shared_rank(aggR.b + jc, q),
-                           *cluster.map_shared_rank(aggR.p + jc, q)};
-                Rcarry = combine(Rcarry, x, (double)chunk_steps(T, t_round + (int64_t)q * Ts, Ts) * jw2);
-            }
+            chunk.put2(warp * kBwdPitch + col, loc[0], loc[1]);
         }
         __syncthreads();
 
-        // 5. the last walk, downwards
-        St R[2];
+        // 4. (P, Q) at every chunk's end, the same from the other side
+        {
+            const int i0 = 2 * part * kBwdPitch + jc, i1 = i0 + kBwdPitch;
+            const Sum x1 = chunk.get(i1);
+            Sum y = join(x1, chunk.get(i0), dL);
+            Sum o = lane_sum<P>(y, part + 1);
+            if (part < P - 1) y = join(o, y, d2);
+            if constexpr (P == 4) {
+                o = lane_sum<P>(y, part + 2);
+                if (part < P - 2) y = join(o, y, d4);
+            }
+            const Sum total = lane_sum<P>(y, 0);
+            Sum ex = lane_sum<P>(y, part + 1);
+            if (part == P - 1) ex = empty_sum();
+            for (int q = rank - 1 - part; q >= 0; q -= P) push_sum(peers, rank * kBwdC + jc, total, bar + 1, q);
+            Sum s = empty_sum();
+            if (part == P - 1) {  // (P, Q) after the round: the last state's, or what rank 0 found last round
+                if (it > 0 && rank > 0) wait(2 + (int)parity, (uint32_t)(it >> 1) & 1 ^ (parity ? 0u : 1u));
+                s = it > 0 ? after.get((int)parity * kBwdC + jc) : Rlast;
+            }
+            if (rank < NC - 1) wait(1, parity);
+            for (int q = q1 - 1; q >= max(q0, rank + 1); --q) s = join(s, peers.get(q * kBwdC + jc), dT);
+            s = decayed(s, d_down);
+#pragma unroll
+            for (int h = 1; h < P; h *= 2) s = join(s, lane_sum<P>(s, part ^ h));
+            if (rank == 0 && round > 0) {  // the round before goes on from this one's start
+                const Sum x = join(s, total, dT), y0 = scaled(x.a, x.b, x.p);
+                const int slot = (int)(parity ^ 1) * kBwdC + jc;
+                if (part == P - 1) after.put(slot, y0);
+                for (int q = 1 + part; q < NC; q += P) push_sum(after, slot, y0, bar + 2 + (parity ^ 1), q);
+            }
+            const Sum R1 = join(s, ex, d_after);
+            chunk.put(i1, R1);
+            chunk.put(i0, join(R1, x1, dL));
+        }
+        __syncthreads();
+
+        // 5. the walk down
+        Sum R[2];
+        chunk.get2(warp * kBwdPitch + col, R);
         bool fastR[2];
-        float p0[2], q0[2];
-        const int64_t t_next = t0 + L;
-        const double after = (double)chunk_steps(T, t_next, (NW - 1 - warp) * L);
+        float p0[2], q0f[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const St x = combine(start.get(col + j), chunk.get(warp * kBwdC + col + j), after * cc.w2[j]);
-            R[j] = scaled(x.a, x.b, x.p);
-            const double lift = R[j].p + (double)ref.kref[j];
-            fastR[j] = fast[j] && lift <= (double)(kFastStateLift * kLog2e);
-            const float sc = ex2((float)lift);
+            if (n < L) R[j] = decayed(R[j], decay_of(rate_of(cc.w[j]), L - n));
+            R[j] = scaled(R[j].a, R[j].b, R[j].p);
+            const int lift = R[j].p + (int)ref.R[j];
+            fastR[j] = fast[j] && lift <= kBwdLift;
+            const float sc = pow2i(min(lift, 127));
             p0[j] = R[j].a * sc;
-            q0[j] = R[j].b * sc;
+            q0f[j] = R[j].b * sc;
         }
-        P = pk(p0[0], p0[1]);
-        Q = pk(q0[0], q0[1]);
-        gw = fma2(P, Ap, fma2(Q, Dp, gw));
+        f2 Pw = pk(p0[0], p0[1]), Qw = pk(q0f[0], q0f[1]);
+        const f2 gw = fma2(Pw, up.Ap, fma2(Qw, up.Dp, up.gw));
         IO* const gk = static_cast<IO*>(p.gk) + at + c;
         IO* const gv = static_cast<IO*>(p.gv) + at + c;
-#pragma unroll 4
-        for (int i = n - 1; i >= 0; --i) {
-            const f2 e = ex2_2(fma2(Pair<IO>::load(sk + i * kBwdC + col), l2e, nref));
-            const f2 v = Pair<IO>::load(sv + i * kBwdC + col);
-            const f2 al = *reinterpret_cast<const f2*>(sal + i * kBwdC + col);
-            const f2 ny = *reinterpret_cast<const f2*>(sy + i * kBwdC + col) ^ 0x8000000080000000ull;
-            const f2 ea = mul2(cc.eu, al);
-            store_pair(gv + (int64_t)i * C, mul2(e, add2(ea, P)), p.vec_store, ok0 && fastR[0],
-                       ok1 && fastR[1]);
-            store_pair(gk + (int64_t)i * C, mul2(e, fma2(ea, add2(v, ny), fma2(P, v, Q))),
-                       p.vec_store, ok0 && fastR[0], ok1 && fastR[1]);
-            P = fma2(cc.ew, P, al);
-            Q = fma2(cc.ew, Q, mul2(al, ny));
-        }
-        float gwj[2] = {lo(gw), hi(gw)}, guj[2] = {lo(gu), hi(gu)};
-        const float Pe[2] = {lo(P), hi(P)}, Qe[2] = {lo(Q), hi(Q)};
+        if (plain && __all_sync(kAll, fastR[0] && fastR[1]))
+            bwd_walk_down<IO, true>(ch, cc, nref, Pw, Qw, gk, gv, C, true, true, true);
+        else
+            bwd_walk_down<IO, false>(ch, cc, nref, Pw, Qw, gk, gv, C, p.vec_store, ok0 && fastR[0],
+                                     ok1 && fastR[1]);
+        float gwj[2] = {lo(gw), hi(gw)}, guj[2] = {lo(up.gu), hi(up.gu)};
+        const float Pe[2] = {lo(Pw), hi(Pw)}, Qe[2] = {lo(Qw), hi(Qw)};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const bool ok = j ? ok1 : ok0;
-            if (n > 0 && ok) {
-                if (fastR[j]) {
-                    R[j] = {Pe[j], Qe[j], -(double)ref.kref[j]};
-                } else {
-                    const ExactGrads x = exact_backward_down<IO>(exact_chunk(j), R[j], gk + j, gv + j);
-                    R[j] = x.R;
-                    gwj[j] = x.gw;
-                    guj[j] = x.gu;
-                }
+            const bool ok = n > 0 && (j ? ok1 : ok0);
+            if (ok && !fastR[j]) {
+                const ExactGrads x = exact_backward_down<IO>(exact_chunk(j), st_of(R[j]), gk + j, gv + j);
+                R[j] = sum_of(x.R.a, x.R.b, x.R.p);
+                gwj[j] = x.gw;
+                guj[j] = x.gu;
             } else {
-                gwj[j] = guj[j] = 0.f;
+                R[j] = {Pe[j], Qe[j], -(int)ref.R[j]};
             }
+            if (!ok) gwj[j] = guj[j] = 0.f;
             if (t0 == 0 && ok && p.gstate_in) {
-                const int64_t ch = b * C + c + j;
-                const double f = exp2(fmin(R[j].p + (double)p.state_in[2 * BC + ch] * kLog2eD, 1000.0));
+                const int64_t sc = (int64_t)b * C + c + j;
+                const double f =
+                    exp2(fmin((double)R[j].p + (double)p.state_in[2 * BC + sc] * kLog2eD, 1000.0));
                 const float ga = (float)(f * R[j].a), gb = (float)(f * R[j].b);
-                const float sa = p.state_in[ch], sb = p.state_in[BC + ch];
-                p.gstate_in[ch] = ga;
-                p.gstate_in[BC + ch] = gb;
-                p.gstate_in[2 * BC + ch] = fmaf(sa, ga, sb * gb);
+                const float sa = p.state_in[sc], sb = p.state_in[BC + sc];
+                p.gstate_in[sc] = ga;
+                p.gstate_in[BC + sc] = gb;
+                p.gstate_in[2 * BC + sc] = fmaf(sa, ga, sb * gb);
             }
         }
         gw_sum = add2(gw_sum, pk(gwj[0], gwj[1]));
         gu_sum = add2(gu_sum, pk(guj[0], guj[1]));
+        __syncwarp();  // the chunk's rows are free for the next round's copies
     }
 
     // the CTA's sums of gw, gu
+    tmem_fence_before_sync();
     __syncthreads();
-    float* const red = reinterpret_cast<float*>(smem + lay.chunks());  // [2][NW][64]
+    tmem_fence_after_sync();
+    float* const red = reinterpret_cast<float*>(smem);  // [2][NW][64], over the rows
     *reinterpret_cast<f2*>(red + warp * kBwdC + col) = gw_sum;
     *reinterpret_cast<f2*>(red + (NW + warp) * kBwdC + col) = gu_sum;
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * kBwdC; i += blockDim.x) {
-        const int which = i / kBwdC, ch = i % kBwdC;
-        if (c0 + ch < C) {
+    for (int i = threadIdx.x; i < 2 * kBwdC; i += 32 * NW) {
+        const int which = i / kBwdC, ci = i % kBwdC;
+        if (c0 + ci < C) {
             float s = 0.f;
-            for (int q = 0; q < NW; ++q) s += red[(which * NW + q) * kBwdC + ch];
-            (which ? p.part_u : p.part_w)[(b * NC + rank) * C + c0 + ch] = s;
+#pragma unroll
+            for (int q = 0; q < NW; ++q) s += red[(which * NW + q) * kBwdC + ci];
+            (which ? p.part_u : p.part_w)[((int64_t)b * NC + rank) * C + c0 + ci] = s;
         }
     }
-    cluster.sync();  // no CTA leaves while a peer may still read its aggregates
+    // (the barriers above are behind every warp's last access to tensor memory)
+    if (warp == 0) tmem_dealloc(*tslot, Lay::kColumns);
+    // every sum pushed to this CTA has been waited for, so it may leave
 }
 
 // Summary of every round's k, v (several rounds): CTA (tile, round), each
 // warp walking its NC chunks of L steps with the next chunk's rows in flight.
 template <typename IO>
-__global__ void __launch_bounds__(256) wkv4_backward_summary_kernel(const BwdParams p, int NC) {
+__global__ void __launch_bounds__(32 * kBwdWarps) wkv4_backward_summary_kernel(const BwdParams p, int NC) {
     allow_dependents();
     grid_dependency_wait();
-    constexpr int L = kBwdL, kTile = BwdLayout<IO>::kTile;
+    constexpr int NW = kBwdWarps, L = kBwdL<IO>, kTile = BwdLayout<IO, false>::kTile;
     extern __shared__ __align__(16) unsigned char smem[];
-    const int NW = blockDim.x >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 2 * lane;
-    const int64_t tile = blockIdx.x, round = blockIdx.y;
-    const int64_t b = tile / p.CGB, c0 = (tile - b * p.CGB) * kBwdC;
-    const int64_t T = p.T, C = p.C, BC = p.B * C;
-    const int64_t t_round = round * NC * NW * L, t_warp = t_round + (int64_t)warp * NC * L;
+    const int round = blockIdx.y, b = blockIdx.z, c0 = (int)blockIdx.x * kBwdC, T = (int)p.T;
+    const int64_t C = p.C, BC = p.B * C;
+    const int t_warp = (round * NW + warp) * NC * L;
     if (!in_range(b, p.B)) return;
-    PairConsts cc;
-    pair_consts(p.w, p.u, c0 + col, C, cc);
+    const BwdConsts cc(p.w, p.u, c0 + col, C);
     unsigned char* const buf = smem + (size_t)warp * 4 * kTile;  // two stages of k, v
-    const Triples chunk(smem + (size_t)NW * 4 * kTile, NW);
+    const Sums chunk(smem + (size_t)NW * 4 * kTile, NW * kBwdC);
     auto load = [&](int q) {
-        const int64_t t = t_warp + (int64_t)q * L;
+        const int t = t_warp + q * L;
         const int n = q < NC ? chunk_steps(T, t, L) : 0;
         unsigned char* const d = buf + (q & 1) * 2 * kTile;
         if (n > 0) {
-            const int64_t at = (b * T + t) * C;
+            const int64_t at = ((int64_t)b * T + t) * C;
             load_rows<IO>(d, static_cast<const IO*>(p.k) + at, C, c0, n, lane, p.vec_load);
             load_rows<IO>(d + kTile, static_cast<const IO*>(p.v) + at, C, c0, n, lane, p.vec_load);
         }
         cp_async_commit();
     };
-    St acc[2] = {empty_state(), empty_state()};
+    const Decay dL[2] = {decay_of(rate_of(cc.w[0]), L), decay_of(rate_of(cc.w[1]), L)};
+    Sum acc[2] = {empty_sum(), empty_sum()};
     load(0);
     for (int q = 0; q < NC; ++q) {
         load(q + 1);
         cp_async_wait<1>();
         __syncwarp();
-        const int n = chunk_steps(T, t_warp + (int64_t)q * L, L);
+        const int n = chunk_steps(T, t_warp + q * L, L);
         const IO* const sk = reinterpret_cast<const IO*>(buf + (q & 1) * 2 * kTile);
-        PairRef ref;
-        St sum[2];
-        chunk_phase1<IO, L>(ref, sk, sk + kTile / sizeof(IO), kBwdC, col, n, cc, sum);
+        BwdRef ref;
+        Sum sum[2];
+        bwd_summary_n<IO>(sk, sk + kTile / sizeof(IO), col, n, cc, ref, sum);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[j] = combine(acc[j], sum[j], (double)n * cc.w2[j]);
+        for (int j = 0; j < 2; ++j) acc[j] = join(acc[j], sum[j], dL[j]);  // nothing follows a cut chunk
         __syncwarp();  // read by every lane before the stage is loaded again
     }
-    chunk.put(warp * kBwdC + col, acc[0]);
-    chunk.put(warp * kBwdC + col + 1, acc[1]);
+    chunk.put2(warp * kBwdC + col, acc[0], acc[1]);
     __syncthreads();
     const int jc = threadIdx.x;
     if (jc < kBwdC && c0 + jc < C) {
-        const double w2 = (double)p.w[c0 + jc] * kLog2eD;
-        St s = empty_state();
-        for (int q = 0; q < NW; ++q)
-            s = combine(s, chunk.get(q * kBwdC + jc),
-                        (double)chunk_steps(T, t_round + (int64_t)q * NC * L, NC * L) * w2);
-        const int64_t i = round * BC + b * C + c0 + jc;
+        const Decay d = decay_of(rate_of(p.w[c0 + jc]), NC * L);
+        Sum s = empty_sum();
+        for (int q = 0; q < NW; ++q) s = join(s, chunk.get(q * kBwdC + jc), d);
+        const int64_t i = (int64_t)round * BC + (int64_t)b * C + c0 + jc;
         p.ck_a[i] = s.a;
         p.ck_b[i] = s.b;
         p.ck_p[i] = s.p;
@@ -680,11 +1014,12 @@ __global__ void __launch_bounds__(128) wkv4_backward_prefix_kernel(const BwdPara
     const int64_t BC = p.B * p.C;
     const int64_t ch = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (ch >= BC) return;
-    const double w2 = (double)p.w[ch % p.C] * kLog2eD;
-    St s = p.state_in ? load_state_log2(p.state_in, BC, ch) : empty_state();
+    const Decay d = decay_of(rate_of(p.w[ch % p.C]), (int)round_steps);
+    Sum s = empty_sum();
+    if (p.state_in) s = sum_of(p.state_in[ch], p.state_in[BC + ch], (double)p.state_in[2 * BC + ch] * kLog2eD);
     constexpr int kAhead = 8;  // rounds loaded at once: the chain waits for memory once per group
     for (int r0 = 0; r0 < p.rounds; r0 += kAhead) {
-        St x[kAhead];
+        Sum x[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int64_t i = (int64_t)(r0 + j) * BC + ch;
@@ -698,10 +1033,31 @@ __global__ void __launch_bounds__(128) wkv4_backward_prefix_kernel(const BwdPara
                 p.ck_b[i] = s.b;
                 p.ck_p[i] = s.p;
                 // every round but the last is whole, and nothing follows the last
-                s = combine(s, x[j], (double)round_steps * w2);
+                s = join(s, x[j], d);
+                s = scaled(s.a, s.b, s.p);
             }
         }
     }
+}
+
+// No steps: the state passes through, and its gradient with it (in the unit of
+// the state given; the two maxima are the same where state_out is a copy).
+__global__ void __launch_bounds__(128) wkv4_backward_no_steps_kernel(const BwdParams p, float* gw, float* gu) {
+    allow_dependents();
+    grid_dependency_wait();
+    const int64_t BC = p.B * p.C;
+    const int64_t ch = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (ch < p.C) gw[ch] = gu[ch] = 0.f;
+    if (ch >= BC || !p.gstate_in) return;
+    float ga = 0.f, gb = 0.f;
+    if (p.gstate_out) {
+        const float f = expf((float)((double)p.state_in[2 * BC + ch] - (double)p.state_out[2 * BC + ch]));
+        ga = f * p.gstate_out[ch];
+        gb = f * p.gstate_out[BC + ch];
+    }
+    p.gstate_in[ch] = ga;
+    p.gstate_in[BC + ch] = gb;
+    p.gstate_in[2 * BC + ch] = fmaf(p.state_in[ch], ga, p.state_in[BC + ch] * gb);
 }
 
 // out[j][c] = sum over rows of part[j][row][c]: up to three column sums, a CTA

@@ -12,16 +12,16 @@
 namespace wkv4 {
 
 // Launch shape of the backward pass, from T and the type alone (the workspace
-// is sized from it): warps a CTA, CTAs a cluster, rounds.
+// is sized from it): CTAs a cluster, rounds.
 struct BwdShape {
-    int NW, NC;
+    int NC;
     int64_t rounds;
 };
 
 static BwdShape bwd_shape(int64_t T, int dtype) {
     BwdShape s;
-    s.NW = dtype == WKV4_F32 || T <= 4 * kBwdL ? 4 : 8;
-    const int64_t ctas = std::max<int64_t>(1, (T + s.NW * kBwdL - 1) / (s.NW * kBwdL));
+    const int64_t steps = kBwdWarps * (dtype == WKV4_F32 ? kBwdL<float> : kBwdL<__half>);
+    const int64_t ctas = std::max<int64_t>(1, (T + steps - 1) / steps);
     s.NC = 1;
     while (s.NC < 8 && s.NC < ctas) s.NC *= 2;
     s.rounds = (ctas + s.NC - 1) / s.NC;
@@ -37,7 +37,7 @@ static size_t bwd_part_bytes(int64_t B, int64_t C, const BwdShape& s) {
 
 size_t backward_workspace(int64_t B, int64_t T, int64_t C, int dtype) {
     const BwdShape s = bwd_shape(T, dtype);
-    return bwd_part_bytes(B, C, s) + (s.rounds > 1 ? (size_t)s.rounds * B * C * 16 : 0);
+    return bwd_part_bytes(B, C, s) + (s.rounds > 1 ? (size_t)s.rounds * B * C * kSumBytes : 0);
 }
 
 static cudaError_t launch_column_sum(const float* part, float* o0, float* o1, float* o2, int n,
@@ -49,31 +49,31 @@ static cudaError_t launch_column_sum(const float* part, float* o0, float* o1, fl
 
 template <typename IO, bool kGate>
 static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdShape& sh) {
-    const BwdLayout<IO> lay{sh.NW};
+    using Lay = BwdLayout<IO, kGate>;
     auto kern = wkv4_backward_kernel<IO, kGate>;
     static DeviceFlags attr;
-    cudaError_t e = ensure_smem_attr(attr, kern, BwdLayout<IO>{8}.bytes());
+    cudaError_t e = ensure_smem_attr(attr, kern, Lay::kBytes);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = a.B * p.CGB;
+    const unsigned tiles = (unsigned)((a.C + kBwdC - 1) / kBwdC), threads = 32 * kBwdWarps;
     if (sh.rounds > 1) {
         auto sum = wkv4_backward_summary_kernel<IO>;
-        const size_t smem = (size_t)sh.NW * (4 * BwdLayout<IO>::kTile + kBwdC * 16);
+        const size_t smem = kBwdWarps * (4 * Lay::kTile + kBwdC * kSumBytes);
         static DeviceFlags sattr;
-        e = ensure_smem_attr(sattr, sum, (size_t)8 * (4 * BwdLayout<IO>::kTile + kBwdC * 16));
+        e = ensure_smem_attr(sattr, sum, smem);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(sum, launch_grid(dim3((unsigned)tiles, (unsigned)sh.rounds)), dim3(32 * sh.NW),
+        e = launch_pdl(sum, launch_grid(dim3(tiles, (unsigned)sh.rounds, (unsigned)a.B)), dim3(threads),
                        smem, a.stream, p, sh.NC);
         if (e != cudaSuccess) return e;
         const int64_t BC = a.B * a.C;
         e = launch_pdl(wkv4_backward_prefix_kernel, launch_grid(dim3((unsigned)((BC + 127) / 128))),
-                       dim3(128), 0, a.stream, p, (int64_t)sh.NC * sh.NW * kBwdL);
+                       dim3(128), 0, a.stream, p, (int64_t)sh.NC * kBwdWarps * kBwdL<IO>);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = launch_grid(dim3((unsigned)(tiles * sh.NC)));
-    cfg.blockDim = dim3(32 * sh.NW);
-    cfg.dynamicSmemBytes = lay.bytes();
+    cfg.gridDim = launch_grid(dim3(tiles * (unsigned)sh.NC, (unsigned)a.B));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = Lay::kBytes;
     cfg.stream = a.stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -91,13 +91,17 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
     return e;
 }
 
+template <typename IO>
+static cudaError_t launch_backward_io(const BwdArgs& a, BwdParams& p, const BwdShape& sh) {
+    return a.r ? launch_backward_t<IO, true>(a, p, sh) : launch_backward_t<IO, false>(a, p, sh);
+}
+
 cudaError_t launch_backward(const BwdArgs& a) {
     const BwdShape sh = bwd_shape(a.T, a.dtype);
     BwdParams p{};
     p.B = a.B;
     p.T = a.T;
     p.C = a.C;
-    p.CGB = (int)((a.C + kBwdC - 1) / kBwdC);
     p.rounds = (int)sh.rounds;
     p.w = a.w;
     p.u = a.u;
@@ -123,22 +127,24 @@ cudaError_t launch_backward(const BwdArgs& a) {
     }
     if (sh.rounds > 1) {
         const int64_t n = sh.rounds * a.B * a.C;
-        p.ck_p = reinterpret_cast<double*>(ws);
-        p.ck_a = reinterpret_cast<float*>(ws + n * 8);
+        p.ck_p = reinterpret_cast<int*>(ws);
+        p.ck_a = reinterpret_cast<float*>(ws + n * 4);
         p.ck_b = p.ck_a + n;
     }
     const size_t es = dtype_size(a.dtype);
     p.vec_load = (a.C * es) % 16 == 0 && aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.gy, 16) &&
                  aligned(a.r, 16);
     p.vec_store = a.C % 2 == 0 && aligned(a.gk, 2 * es) && aligned(a.gv, 2 * es) && aligned(a.gr, 2 * es);
+    p.wait_rounds = wait_rounds();
+    if (a.T == 0) {
+        const int64_t n = a.B * a.C;
+        return launch_pdl(wkv4_backward_no_steps_kernel, launch_grid(dim3((unsigned)((n + 127) / 128))),
+                          dim3(128), 0, a.stream, p, a.gw, a.gu);
+    }
     switch (a.dtype) {
-        case WKV4_F32:
-            return a.r ? launch_backward_t<float, true>(a, p, sh) : launch_backward_t<float, false>(a, p, sh);
-        case WKV4_F16:
-            return a.r ? launch_backward_t<__half, true>(a, p, sh) : launch_backward_t<__half, false>(a, p, sh);
-        default:
-            return a.r ? launch_backward_t<__nv_bfloat16, true>(a, p, sh)
-                       : launch_backward_t<__nv_bfloat16, false>(a, p, sh);
+        case WKV4_F32: return launch_backward_io<float>(a, p, sh);
+        case WKV4_F16: return launch_backward_io<__half>(a, p, sh);
+        default: return launch_backward_io<__nv_bfloat16>(a, p, sh);
     }
 }
 
