@@ -57,6 +57,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "wkv4_chunk.cuh"
 
 namespace wkv4 {
@@ -85,14 +87,15 @@ struct BwdParams {
     void* gv;
     void* gr;
     float* gstate_in;  // [3][B][C] or NULL
-    float* part_w;     // [rows][C] partial sums, row b NC + rank
+    float* part_w;     // [rows][C] partial sums, row (grid y) NC + rank
     float* part_u;
     // rounds > 1: per round and channel the summary, then the state at the round's start
     int* ck_p;         // [rounds][B C]
     float* ck_a;
     float* ck_b;
     uint32_t wait_rounds;  // limit of each bounded wait
-    bool vec_load;     // every row starts on 16 bytes
+    int nb;            // batch rows a cluster walks, one after another
+    bool vec_load;     // every row of k, v, gout, r starts on 16 bytes
     bool vec_store;    // channel pairs of gk, gv, gr may be stored as one access
 };
 
@@ -240,24 +243,25 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int by
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's n rows of 64 channels from c0 of one [B][T][C] tensor (src: batch
-// row b, step t0, channel 0) into shared memory; channels past C read as
-// zero, rows past n are left.  vec: C and the base are multiples of 16 bytes,
-// 16-byte asynchronous copies; otherwise element by element.
+// A warp's n rows of 64 channels from c0 of a [B][T][C] tensor (src: the first
+// row, channel 0) into shared memory; channels past C read as zero, rows past
+// n are left.  vec: every row starts on 16 bytes, 16-byte asynchronous copies;
+// otherwise element by element.
 template <typename IO>
-__device__ __forceinline__ void load_rows(unsigned char* dst, const IO* src, int64_t C, int64_t c0,
-                                          int n, int lane, bool vec) {
+__device__ __forceinline__ void load_rows(unsigned char* dst, const IO* src, int64_t C, int c0, int n,
+                                          int lane, bool vec) {
     constexpr int kE = 16 / (int)sizeof(IO), kP = kBwdC / kE;  // elements a piece, pieces a row
     if (vec) {
         constexpr int kR = 32 / kP;  // rows a pass of the warp
         const int row = lane / kP, piece = lane % kP;
-        const int64_t c = c0 + piece * kE;
+        const int c = c0 + piece * kE;
         const int bytes = c < C ? 16 : 0;
         const uint32_t d = smem_u32(dst) + (uint32_t)(row * kBwdC * (int)sizeof(IO) + piece * 16);
         const IO* s = src + (int64_t)row * C + (c < C ? c : 0);
@@ -267,14 +271,25 @@ __device__ __forceinline__ void load_rows(unsigned char* dst, const IO* src, int
             s += (int64_t)kR * C;
         }
     } else {
-        IO* d = reinterpret_cast<IO*>(dst);
-        for (int row = 0; row < n; ++row)
+        IO* d = reinterpret_cast<IO*>(dst) + lane;
+        const IO* s = src + c0 + lane;
+        const bool ok0 = c0 + lane < C, ok1 = c0 + lane + 32 < C;
+        constexpr int kG = 8;  // rows in flight
+#pragma unroll 1
+        for (int q = 0; q < n; q += kG) {
+            IO x[kG][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int j = lane + 32 * h;
-                const int64_t c = c0 + j;
-                d[row * kBwdC + j] = c < C ? src[(int64_t)row * C + c] : Io<IO>::from_f(0.f);
+            for (int i = 0; i < kG; ++i) {
+                x[i][0] = ok0 && q + i < n ? s[(int64_t)i * C] : Io<IO>::from_f(0.f);
+                x[i][1] = ok1 && q + i < n ? s[(int64_t)i * C + 32] : Io<IO>::from_f(0.f);
             }
+#pragma unroll
+            for (int i = 0; i < kG; ++i) {
+                d[(q + i) * kBwdC] = x[i][0];
+                d[(q + i) * kBwdC + 32] = x[i][1];
+            }
+            s += (int64_t)kG * C;
+        }
     }
 }
 
@@ -395,6 +410,17 @@ __device__ __forceinline__ void store_pair(IO* p, f2 x, bool vec, bool ok0, bool
     }
 }
 
+// A stored pair as floats.  bf16: the halves of a float's bits, two operations.
+template <typename IO>
+__device__ __forceinline__ f2 load_f2(const IO* p) {
+    if constexpr (std::is_same<IO, __nv_bfloat16>::value) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+        return pku(x << 16, x & 0xffff0000u);
+    } else {
+        return Pair<IO>::load(p);
+    }
+}
+
 constexpr f2 kSigns = 0x8000000080000000ull;
 
 // A pair's decay and bonus.
@@ -419,15 +445,17 @@ struct BwdRef {
     bool fast[2];
 };
 
-// The chunk's sums from the empty state.
-template <typename IO, bool kFull>
+// The chunk's sums from the empty state (n >= 0 steps).
+template <typename IO>
 __device__ __forceinline__ void bwd_summary(const IO* sk, const IO* sv, int col, int n,
                                             const BwdConsts& cc, BwdRef& ref, Sum (&sum)[2]) {
-    constexpr int L = kBwdL<IO>;
+    sum[0] = sum[1] = empty_sum();
+    ref.fast[0] = ref.fast[1] = false;
+    ref.R[0] = ref.R[1] = 0.f;
+    if (n == 0) return;
     typename Pair<IO>::Raw mx = Pair<IO>::raw(sk + col), mn = mx;
-#pragma unroll
-    for (int i = 1; i < L; ++i)
-        if (kFull || i < n) Pair<IO>::minmax(Pair<IO>::raw(sk + i * kBwdC + col), mx, mn);
+#pragma unroll 8
+    for (int i = 1; i < n; ++i) Pair<IO>::minmax(Pair<IO>::raw(sk + i * kBwdC + col), mx, mn);
     float kmax[2], kmin[2];
     Pair<IO>::bounds(mx, mn, kmax, kmin);
 #pragma unroll
@@ -439,13 +467,11 @@ __device__ __forceinline__ void bwd_summary(const IO* sk, const IO* sv, int col,
     }
     const f2 l2e = pk(kLog2e, kLog2e), nref = pk(-ref.R[0], -ref.R[1]);
     f2 A = 0ull, D = 0ull;
-#pragma unroll
-    for (int i = 0; i < L; ++i) {
-        if (kFull || i < n) {
-            const f2 e = ex2_2(fma2(Pair<IO>::load(sk + i * kBwdC + col), l2e, nref));
-            A = fma2(e, Pair<IO>::load(sv + i * kBwdC + col), mul2(cc.ew, A));
-            D = fma2(cc.ew, D, e);
-        }
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        const f2 e = ex2_2(fma2(load_f2<IO>(sk + i * kBwdC + col), l2e, nref));
+        A = fma2(e, load_f2<IO>(sv + i * kBwdC + col), mul2(cc.ew, A));
+        D = fma2(cc.ew, D, e);
     }
     const float Aj[2] = {lo(A), hi(A)}, Dj[2] = {lo(D), hi(D)};
 #pragma unroll
@@ -458,20 +484,6 @@ __device__ __forceinline__ void bwd_summary(const IO* sk, const IO* sv, int col,
             const St x = slow_summary<IO>(sk + col + j, sv + col + j, kBwdC, n, (double)cc.w[j] * kLog2eD);
             sum[j] = sum_of(x.a, x.b, x.p);
         }
-    }
-}
-
-template <typename IO>
-__device__ __forceinline__ void bwd_summary_n(const IO* sk, const IO* sv, int col, int n,
-                                              const BwdConsts& cc, BwdRef& ref, Sum (&sum)[2]) {
-    if (n >= kBwdL<IO>) {
-        bwd_summary<IO, true>(sk, sv, col, n, cc, ref, sum);
-    } else if (n > 0) {
-        bwd_summary<IO, false>(sk, sv, col, n, cc, ref, sum);
-    } else {
-        sum[0] = sum[1] = empty_sum();
-        ref.fast[0] = ref.fast[1] = false;
-        ref.R[0] = ref.R[1] = 0.f;
     }
 }
 
@@ -521,39 +533,38 @@ struct BwdUp {
 // for it; 2^98 times a gradient of 2^29 is still in range.
 constexpr int kUpShift = 40;
 
-// Step 3.  kPlain: a whole chunk, every lane's two channels on the
-// fixed-reference path, rows stored as pairs.
+// Step 3.  kPlain: a whole chunk with every lane's two channels present, on the
+// fixed-reference path and stored as pairs.
 template <typename IO, bool kGate, bool kPlain>
 __device__ __forceinline__ void bwd_walk_up(const BwdChunk<IO>& ch, const BwdConsts& cc, f2 nref, f2 A,
                                             f2 D, IO* gr, int64_t C, bool vec, bool s0, bool s1, BwdUp& o) {
     const f2 l2e = pk(kLog2e, kLog2e), one = pk(1.f, 1.f), m1 = pk(-1.f, -1.f);
     f2 Ap = 0ull, Dp = 0ull, gw = 0ull, gu = 0ull, P = 0ull, Q = 0ull;
     f2 f = pk(0x1p40f, 0x1p40f);
-#pragma unroll(kPlain ? 2 : 1)
+#pragma unroll 1
     for (int q = 0; q < (kPlain ? kBwdL<IO> : ch.n); q += 4) {
         uint32_t st[16];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             const int i = q + s;
             if (kPlain || i < ch.n) {
-                const f2 e = ex2_2(fma2(Pair<IO>::load(ch.k + i * kBwdC + ch.col), l2e, nref));
-                const f2 v = Pair<IO>::load(ch.v + i * kBwdC + ch.col);
+                const f2 e = ex2_2(fma2(load_f2<IO>(ch.k + i * kBwdC + ch.col), l2e, nref));
+                const f2 v = load_f2<IO>(ch.v + i * kBwdC + ch.col);
                 const f2 ee = mul2(cc.eu, e);
                 const f2 rz = rcp2(add2(D, ee));
                 const f2 ny = mul2(mul2(fma2(ee, v, A), m1), rz);
-                f2 g = Pair<IO>::load(ch.gy + i * kBwdC + ch.col);
+                f2 g = load_f2<IO>(ch.gy + i * kBwdC + ch.col);
                 if constexpr (kGate) {
-                    const f2 x0 = mul2(Pair<IO>::load(ch.r + i * kBwdC + ch.col), pk(-kLog2e, -kLog2e));
+                    const f2 x0 = mul2(load_f2<IO>(ch.r + i * kBwdC + ch.col), pk(-kLog2e, -kLog2e));
                     // (above 2^126 the gate is 0 to within its rounding, and x s stays finite)
                     const f2 x = pk(ex2(fminf(lo(x0), 126.f)), ex2(fminf(hi(x0), 126.f)));
                     const f2 sg = rcp2(add2(one, x));
                     g = mul2(g, sg);
                     const f2 grv = mul2(mul2(g, ny), mul2(x, sg)) ^ kSigns;
                     if constexpr (kPlain)
-                        Pair<IO>::store(gr, grv);
+                        Pair<IO>::store(gr + (int64_t)i * C, grv);
                     else
-                        store_pair(gr, grv, vec, s0, s1);
-                    gr += C;
+                        store_pair(gr + (int64_t)i * C, grv, vec, s0, s1);
                 }
                 const f2 al = mul2(g, rz);
                 const f2 nay = mul2(al, ny);
@@ -589,8 +600,6 @@ __device__ __forceinline__ void bwd_walk_down(const BwdChunk<IO>& ch, const BwdC
                                               f2& Q, IO* gk, IO* gv, int64_t C, bool vec, bool s0, bool s1) {
     const f2 l2e = pk(kLog2e, kLog2e);
     const int n = kPlain ? kBwdL<IO> : ch.n;
-    gk += (int64_t)(n - 1) * C;
-    gv += (int64_t)(n - 1) * C;
 #pragma unroll 1
     for (int q = (n - 1) & ~7; q >= 0; q -= 8) {
         uint32_t st[32];
@@ -600,20 +609,18 @@ __device__ __forceinline__ void bwd_walk_down(const BwdChunk<IO>& ch, const BwdC
         for (int s = 7; s >= 0; --s) {
             const int i = q + s;
             if (kPlain || i < n) {
-                const f2 e = ex2_2(fma2(Pair<IO>::load(ch.k + i * kBwdC + ch.col), l2e, nref));
-                const f2 v = Pair<IO>::load(ch.v + i * kBwdC + ch.col);
+                const f2 e = ex2_2(fma2(load_f2<IO>(ch.k + i * kBwdC + ch.col), l2e, nref));
+                const f2 v = load_f2<IO>(ch.v + i * kBwdC + ch.col);
                 const f2 al = pku(st[4 * s], st[4 * s + 1]), nay = pku(st[4 * s + 2], st[4 * s + 3]);
                 const f2 h = fma2(cc.eu, al, P), j = fma2(cc.eu, nay, Q);
                 const f2 xv = mul2(e, h), xk = mul2(e, fma2(h, v, j));
                 if constexpr (kPlain) {
-                    Pair<IO>::store(gv, xv);
-                    Pair<IO>::store(gk, xk);
+                    Pair<IO>::store(gv + (int64_t)i * C, xv);
+                    Pair<IO>::store(gk + (int64_t)i * C, xk);
                 } else {
-                    store_pair(gv, xv, vec, s0, s1);
-                    store_pair(gk, xk, vec, s0, s1);
+                    store_pair(gv + (int64_t)i * C, xv, vec, s0, s1);
+                    store_pair(gk + (int64_t)i * C, xk, vec, s0, s1);
                 }
-                gv -= C;
-                gk -= C;
                 P = fma2(cc.ew, P, al);
                 Q = fma2(cc.ew, Q, nay);
             }
@@ -634,44 +641,59 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     cg::cluster_group cluster = cg::this_cluster();
     const int NC = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 2 * lane;
-    const int b = blockIdx.y, c0 = (int)(blockIdx.x >> (__ffs(NC) - 1)) * kBwdC;
-    const int T = (int)p.T;
+    const int c0 = (int)(blockIdx.x >> (__ffs(NC) - 1)) * kBwdC;
+    const int T = (int)p.T, rounds = p.rounds, last = rounds - 1;
     const int64_t C = p.C, BC = p.B * C;
     const int round_steps = NC * Ts;
     const int64_t c = c0 + col;
     const bool ok0 = c < C, ok1 = c + 1 < C;
-    // every global access below is (b T + t) C + c for t < T, c < C, or b C + c
-    if (!in_range(b, p.B)) return;
-    const int64_t row0 = (int64_t)b * T;
+    // the batch rows of this cluster, each walked from its last round to its first
+    const int b0 = blockIdx.y * p.nb, items = min(p.nb, (int)p.B - b0) * rounds;
+    // every global access below is (b T + t) C + c for b < B, t < T, c < C, or b C + c
+    if (!in_range(b0, p.B)) return;
 
     unsigned char* const wbase = smem + warp * Lay::kWarp;
     const Sums chunk(smem + Lay::kChunks, NW * kBwdPitch);
     const Sums peers(smem + Lay::kPeers, kBwdMaxCtas * kBwdC);  // row q: CTA q's sum (below rank forward, above backward)
-    const Sums after(smem + Lay::kCarry, 2 * kBwdC);            // (P, Q) after a round, by the round's parity
+    const Sums after(smem + Lay::kCarry, 2 * kBwdC);            // (P, Q) after a round, two in turn
     // barriers: the lower ranks' forward sums, the higher ranks' (P, Q), the two rows of `after`
     uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + Lay::kBars);
     uint32_t* const tslot = reinterpret_cast<uint32_t*>(bar + 4);
 
-    auto load_chunk = [&](int round) {
+    bool failed = false;  // a bounded wait ran out: go on without waiting (the results are reported bad)
+    auto wait = [&](int which, uint32_t parity) {
+        if (failed || mbar_wait_cluster_bounded(bar + which, parity, p.wait_rounds)) return;
+        atomicOr(&g_device_error, kErrExchangeWait);
+        failed = true;
+    };
+    // an item's rows of this warp: k and v, then (a second group) gout and r
+    auto load_item = [&](int b, int round) {
         const int t0 = round * round_steps + rank * Ts + warp * L;
         const int n = chunk_steps(T, t0, L);
-        if (n > 0) {
-            const int64_t at = (row0 + t0) * C;
-            load_rows<IO>(wbase, static_cast<const IO*>(p.k) + at, C, c0, n, lane, p.vec_load);
-            load_rows<IO>(wbase + Lay::kTile, static_cast<const IO*>(p.v) + at, C, c0, n, lane,
+        const int64_t at = ((int64_t)b * T + t0) * C;
+        const void* const src[4] = {p.k, p.v, p.gy, p.r};
+#pragma unroll
+        for (int q = 0; q < (kGate ? 4 : 3); ++q) {
+            load_rows<IO>(wbase + q * Lay::kTile, static_cast<const IO*>(src[q]) + at, C, c0, n, lane,
                           p.vec_load);
-            cp_async_commit();
-            load_rows<IO>(wbase + 2 * Lay::kTile, static_cast<const IO*>(p.gy) + at, C, c0, n, lane,
-                          p.vec_load);
-            if constexpr (kGate)
-                load_rows<IO>(wbase + 3 * Lay::kTile, static_cast<const IO*>(p.r) + at, C, c0, n,
-                              lane, p.vec_load);
-        } else {
-            cp_async_commit();
+            if (q == 1) cp_async_commit();
         }
         cp_async_commit();
     };
-    load_chunk(p.rounds - 1);
+    // an item's rows of this warp brought to L2 (32 lanes, 128 bytes each)
+    auto prefetch_item = [&](int b, int round) {
+        constexpr int kLanes = 32 / L;
+        const int t = round * round_steps + rank * Ts + warp * L + lane / kLanes;
+        const int cl = c0 + (lane % kLanes) * (kBwdC / kLanes);
+        if (t < T && cl < C) {
+            const int64_t o = ((int64_t)b * T + t) * C + cl;
+            prefetch_l2(static_cast<const IO*>(p.k) + o);
+            prefetch_l2(static_cast<const IO*>(p.v) + o);
+            prefetch_l2(static_cast<const IO*>(p.gy) + o);
+            if constexpr (kGate) prefetch_l2(static_cast<const IO*>(p.r) + o);
+        }
+    };
+    load_item(b0, last);
     if (threadIdx.x < 4) mbar_init(bar + threadIdx.x, 1);
     if (threadIdx.x == 0) fence_mbar_init();
     if (warp == 0) tmem_alloc(tslot, Lay::kColumns);
@@ -689,7 +711,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     // and CTAs q0 .. q0 + qn - 1 of the cluster
     const int jc = threadIdx.x / P, part = threadIdx.x % P;
     const bool jok = c0 + jc < C;
-    const int64_t jch = (int64_t)b * C + c0 + jc;
+    
     const Rate rate = rate_of(jok ? p.w[c0 + jc] : 0.f);
     const Decay dL = decay_of(rate, L), d2 = decay_of(rate, 2 * L), d4 = decay_of(rate, 4 * L),
                 dT = decay_of(rate, Ts);
@@ -699,42 +721,32 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     // of CTA max(q0, rank + 1) to this CTA's end
     const Decay d_up = decay_of(rate, (rank - min(q1, rank)) * Ts);
     const Decay d_down = decay_of(rate, (max(q0, rank + 1) - (rank + 1)) * Ts);
-    const int last = p.rounds - 1;
-    // (P, Q) after the last step, carried on to the end of the last round (as if
-    // the recurrence ran on there): every chunk is then a whole one to the joins
-    Sum Rlast = empty_sum();
-    if (jok && p.gstate_out) {
-        const Sum x = sum_of(p.gstate_out[jch], p.gstate_out[BC + jch],
-                             -(double)p.state_out[2 * BC + jch] * kLog2eD);
-        const int pad = (last + 1) * round_steps - T;
-        const Decay d = decay_of(Rate{-rate.hi, -rate.lo}, pad);
-        Rlast = scaled(x.a * d.f, x.b * d.f, x.p + d.i);
-    }
-    bool failed = false;  // a bounded wait ran out: go on without waiting (the results are reported bad)
-    auto wait = [&](int which, uint32_t parity) {
-        if (failed || mbar_wait_cluster_bounded(bar + which, parity, p.wait_rounds)) return;
-        atomicOr(&g_device_error, kErrExchangeWait);
-        failed = true;
-    };
-
     f2 gw_sum = 0ull, gu_sum = 0ull;
+    int passed = 0;  // rounds handed on so far: `after` and its barriers take turns
 
-    for (int round = last; round >= 0; --round) {
-        const int it = last - round;
+#pragma unroll 1
+    for (int it = 0, b = b0, round = last; it < items; ++it) {
         const uint32_t parity = it & 1;
+        const bool handed = round < last;  // this round goes on from the one after it
         const int t0 = round * round_steps + rank * Ts + warp * L;
         const int n = ch.n = chunk_steps(T, t0, L);
-        const int64_t at = (row0 + t0) * C;  // element offset of the chunk's first row
-        if (it > 0) load_chunk(round);
+        const int64_t at = ((int64_t)b * T + t0) * C;  // element offset of the chunk's first row
+        const int64_t jch = (int64_t)b * C + c0 + jc;
+        if (it > 0) {
+            __syncwarp();  // the last item's rows have been read by every lane
+            load_item(b, round);
+        }
         if (threadIdx.x == 0) {  // what this round's barriers will receive
             if (rank > 0) mbar_arrive_expect_tx(bar, (uint32_t)rank * kBwdC * kSumBytes);
             if (rank < NC - 1) mbar_arrive_expect_tx(bar + 1, (uint32_t)(NC - 1 - rank) * kBwdC * kSumBytes);
-            if (rank > 0 && it > 0) mbar_arrive_expect_tx(bar + 2 + parity, kBwdC * kSumBytes);
+            if (rank > 0 && handed) mbar_arrive_expect_tx(bar + 2 + (passed & 1), kBwdC * kSumBytes);
         }
+        // the next item's rows while this one is waited for
+        if (it + 1 < items) prefetch_item(round > 0 ? b : b + 1, round > 0 ? round - 1 : last);
         // the state at the round's start
         Sum carry = empty_sum();
         if (jok && part == 0) {
-            if (p.rounds > 1) {
+            if (rounds > 1) {
                 const int64_t i = (int64_t)round * BC + jch;
                 carry = {p.ck_a[i], p.ck_b[i], p.ck_p[i]};
             } else if (p.state_in) {
@@ -749,7 +761,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         BwdRef ref;
         {
             Sum sum[2];
-            bwd_summary_n<IO>(ch.k, ch.v, col, n, cc, ref, sum);
+            bwd_summary<IO>(ch.k, ch.v, col, n, cc, ref, sum);
             chunk.put2(warp * kBwdPitch + col, sum[0], sum[1]);
         }
         __syncthreads();
@@ -805,12 +817,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         IO* const gr = kGate ? static_cast<IO*>(p.gr) + at + c : nullptr;
         BwdUp up;
         const bool plain = __all_sync(kAll, n == L && p.vec_store && ok1 && fast[0] && fast[1]);
-        if (plain)
+        if (plain) {
             bwd_walk_up<IO, kGate, true>(ch, cc, nref, pk(a0[0], a0[1]), pk(b0[0], b0[1]), gr, C, true, true,
                                          true, up);
-        else
+        } else {
             bwd_walk_up<IO, kGate, false>(ch, cc, nref, pk(a0[0], a0[1]), pk(b0[0], b0[1]), gr, C,
                                           p.vec_store, ok0 && fast[0], ok1 && fast[1], up);
+        }
         auto exact_chunk = [&](int j) {
             return ExactChunk<IO>{static_cast<const IO*>(p.k) + at + c + j,
                                   static_cast<const IO*>(p.v) + at + c + j,
@@ -852,11 +865,22 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             Sum ex = lane_sum<P>(y, part + 1);
             if (part == P - 1) ex = empty_sum();
             for (int q = rank - 1 - part; q >= 0; q -= P) push_sum(peers, rank * kBwdC + jc, total, bar + 1, q);
+            // (P, Q) after the round: what rank 0 found last round, or the last
+            // state's, carried on to the end of the last round (as if the
+            // recurrence ran on there: every chunk is a whole one to the joins)
             Sum s = empty_sum();
-            if (part == P - 1) {  // (P, Q) after the round: the last state's, or what rank 0 found last round
-                if (it > 0 && rank > 0) wait(2 + (int)parity, (uint32_t)(it >> 1) & 1 ^ (parity ? 0u : 1u));
-                s = it > 0 ? after.get((int)parity * kBwdC + jc) : Rlast;
+            if (part == P - 1) {
+                if (handed) {
+                    if (rank > 0) wait(2 + (passed & 1), (passed >> 1) & 1);
+                    s = after.get((passed & 1) * kBwdC + jc);
+                } else if (jok && p.gstate_out) {
+                    const Sum x = sum_of(p.gstate_out[jch], p.gstate_out[BC + jch],
+                                         -(double)p.state_out[2 * BC + jch] * kLog2eD);
+                    const Decay d = decay_of(Rate{-rate.hi, -rate.lo}, rounds * round_steps - T);
+                    s = scaled(x.a * d.f, x.b * d.f, x.p + d.i);
+                }
             }
+            if (handed) ++passed;
             if (rank < NC - 1) wait(1, parity);
             for (int q = q1 - 1; q >= max(q0, rank + 1); --q) s = join(s, peers.get(q * kBwdC + jc), dT);
             s = decayed(s, d_down);
@@ -864,9 +888,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             for (int h = 1; h < P; h *= 2) s = join(s, lane_sum<P>(s, part ^ h));
             if (rank == 0 && round > 0) {  // the round before goes on from this one's start
                 const Sum x = join(s, total, dT), y0 = scaled(x.a, x.b, x.p);
-                const int slot = (int)(parity ^ 1) * kBwdC + jc;
+                const int slot = (passed & 1) * kBwdC + jc;
                 if (part == P - 1) after.put(slot, y0);
-                for (int q = 1 + part; q < NC; q += P) push_sum(after, slot, y0, bar + 2 + (parity ^ 1), q);
+                for (int q = 1 + part; q < NC; q += P) push_sum(after, slot, y0, bar + 2 + (passed & 1), q);
             }
             const Sum R1 = join(s, ex, d_after);
             chunk.put(i1, R1);
@@ -893,11 +917,12 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         const f2 gw = fma2(Pw, up.Ap, fma2(Qw, up.Dp, up.gw));
         IO* const gk = static_cast<IO*>(p.gk) + at + c;
         IO* const gv = static_cast<IO*>(p.gv) + at + c;
-        if (plain && __all_sync(kAll, fastR[0] && fastR[1]))
+        if (plain && __all_sync(kAll, fastR[0] && fastR[1])) {
             bwd_walk_down<IO, true>(ch, cc, nref, Pw, Qw, gk, gv, C, true, true, true);
-        else
+        } else {
             bwd_walk_down<IO, false>(ch, cc, nref, Pw, Qw, gk, gv, C, p.vec_store, ok0 && fastR[0],
                                      ok1 && fastR[1]);
+        }
         float gwj[2] = {lo(gw), hi(gw)}, guj[2] = {lo(up.gu), hi(up.gu)};
         const float Pe[2] = {lo(Pw), hi(Pw)}, Qe[2] = {lo(Qw), hi(Qw)};
 #pragma unroll
@@ -925,7 +950,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         }
         gw_sum = add2(gw_sum, pk(gwj[0], gwj[1]));
         gu_sum = add2(gu_sum, pk(guj[0], guj[1]));
-        __syncwarp();  // the chunk's rows are free for the next round's copies
+        // the next item: the round before, then the next batch row's last
+        if (round > 0) {
+            --round;
+        } else {
+            round = last;
+            ++b;
+        }
     }
 
     // the CTA's sums of gw, gu
@@ -942,7 +973,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             float s = 0.f;
 #pragma unroll
             for (int q = 0; q < NW; ++q) s += red[(which * NW + q) * kBwdC + ci];
-            (which ? p.part_u : p.part_w)[((int64_t)b * NC + rank) * C + c0 + ci] = s;
+            (which ? p.part_u : p.part_w)[((int64_t)blockIdx.y * NC + rank) * C + c0 + ci] = s;
         }
     }
     // (the barriers above are behind every warp's last access to tensor memory)
@@ -970,11 +1001,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps) wkv4_backward_summary_kernel(c
         const int t = t_warp + q * L;
         const int n = q < NC ? chunk_steps(T, t, L) : 0;
         unsigned char* const d = buf + (q & 1) * 2 * kTile;
-        if (n > 0) {
-            const int64_t at = ((int64_t)b * T + t) * C;
-            load_rows<IO>(d, static_cast<const IO*>(p.k) + at, C, c0, n, lane, p.vec_load);
-            load_rows<IO>(d + kTile, static_cast<const IO*>(p.v) + at, C, c0, n, lane, p.vec_load);
-        }
+        const int64_t at = ((int64_t)b * T + t) * C;
+        load_rows<IO>(d, static_cast<const IO*>(p.k) + at, C, c0, n, lane, p.vec_load);
+        load_rows<IO>(d + kTile, static_cast<const IO*>(p.v) + at, C, c0, n, lane, p.vec_load);
         cp_async_commit();
     };
     const Decay dL[2] = {decay_of(rate_of(cc.w[0]), L), decay_of(rate_of(cc.w[1]), L)};
@@ -988,7 +1017,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) wkv4_backward_summary_kernel(c
         const IO* const sk = reinterpret_cast<const IO*>(buf + (q & 1) * 2 * kTile);
         BwdRef ref;
         Sum sum[2];
-        bwd_summary_n<IO>(sk, sk + kTile / sizeof(IO), col, n, cc, ref, sum);
+        bwd_summary<IO>(sk, sk + kTile / sizeof(IO), col, n, cc, ref, sum);
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[j] = join(acc[j], sum[j], dL[j]);  // nothing follows a cut chunk
         __syncwarp();  // read by every lane before the stage is loaded again
