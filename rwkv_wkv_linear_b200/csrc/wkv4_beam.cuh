@@ -12,31 +12,39 @@
 // own reference, joined over threads and units in fp64), and the unit's n
 // largest logits are found on the way:
 //   * each thread's maximum over its first batch gives a bound: the n-th
-//     largest of the 256 maxima is at most the unit's n-th largest logit;
-//   * elements at or above the bound go to a list in shared memory (about
-//     n times the unit's batches on unordered data), whose n largest are
-//     ranked by counting;
-//   * a list that overflows (many equal logits) is dropped and the n largest
-//     are found one by one, each a pass over the unit.
+//     largest of the 256 maxima is at most the unit's n-th largest logit.  It is
+//     found among the maxima at or above a looser one, the least of the warps'
+//     (n/8)-th largest;
+//   * the 16-byte pieces with an element at or above the bound are noted in
+//     kept in shared memory (about n times the unit's batches on unordered
+//     data), gone through after the pass, and the n largest of what they hold
+//     at or above the bound are ranked by counting;
+//   * where either list overflows (many equal logits) the n largest are found
+//     one by one, each a pass over the unit.
 // Logits of one row order like their scores, so only n a unit matter; the
 // first CTA of the cluster receives the units' lists and sums through cluster
-// shared memory, computes the scores in fp64 and merges the lists' heads, one
-// warp, a lane a unit.
+// shared memory, computes the scores in fp64 and ranks those at or above a
+// bound (the least of the units' (n/units)-th best) by counting.
 //
-// What bounds it: HBM reads of the logits, with one ex2 an element close
-// behind (16 a clock and SM).
+// What bounds it: for a batch the HBM reads of the logits, with one ex2 an
+// element close behind (16 a clock and SM); for one request the chain of
+// latencies: three batches of loads are in flight a thread.
 #pragma once
 
 #include <cooperative_groups.h>
 
-#include "wkv4_device.cuh"
+#include <type_traits>
+
+#include "wkv4_chunk.cuh"  // packed f32x2, Pair
 
 namespace wkv4 {
 
 constexpr int kBeamThreads = 256;
+constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamMaxN = 64;       // candidates a group
 constexpr int kBeamMaxK = 32;       // beams a group: a lane of the merging warp each
-constexpr int kBeamList = 1024;     // elements a unit's list holds
+constexpr int kBeamPieces = 1024;   // pieces with a candidate that a unit's list holds
+constexpr int kBeamList = 1024;     // candidates a unit's list holds
 constexpr int kBeamBatch = 4;       // 16-byte pieces a thread loads at once
 constexpr float kBeamMaxScore = 2e9f;  // |score| of a live beam; beyond, fp64 sums no longer tell logits apart
 
@@ -74,23 +82,62 @@ struct BeamUnit {
     uint64_t keys[kBeamMaxN];
 };
 
-struct BeamShared {
+struct alignas(16) BeamShared {
     BeamUnit units[kBeamMaxK];
-    uint64_t list[kBeamList];
+    alignas(16) uint64_t list[kBeamList + 2];
+    int32_t piece_at[kBeamPieces];
     uint64_t best[kBeamMaxN];
-    float tmax[kBeamThreads];
-    float wref[kBeamThreads / 32];
-    double wsum[kBeamThreads / 32];
-    uint64_t wkey[kBeamThreads / 32];
-    float bound;
-    int count;
+    double lse[kBeamMaxK];
+    alignas(16) uint32_t top[kBeamThreads];  // the threads' first maxima at or above the loose bound
+    uint32_t wbound[kBeamWarps];
+    float wref[kBeamWarps];
+    double wsum[kBeamWarps];
+    uint64_t wkey[kBeamWarps];
+    uint32_t bound;
+    int tops, count, npieces;
+    // then [kBeamPieces] pieces, or in the merge all candidates and those ranked
+    __device__ __forceinline__ uint4* pieces() { return reinterpret_cast<uint4*>(this + 1); }
 };
 
 template <typename IO>
 struct BeamVec {
-    static constexpr int E = 16 / (int)sizeof(IO);
-    static constexpr int N = kBeamBatch * E;
+    static constexpr int E = 16 / (int)sizeof(IO);  // elements of a 16-byte piece
+    // two elements of a piece as floats
+    __device__ __forceinline__ static f2 pair(const uint4& x, int h) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        if constexpr (sizeof(IO) == 4) {
+            return pku(w[2 * h], w[2 * h + 1]);
+        } else if constexpr (std::is_same<IO, __nv_bfloat16>::value) {
+            return pku(w[h] << 16, w[h] & 0xffff0000u);
+        } else {
+            return Pair<__half>::cvt(*reinterpret_cast<const __half2*>(&w[h]));
+        }
+    }
+    // the piece's largest element (NaN left out)
+    __device__ __forceinline__ static float max(const uint4& x) {
+        if constexpr (sizeof(IO) == 4) {
+            return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)),
+                         fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+        } else {
+            typedef typename Pair<IO>::Raw Raw;
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            Raw r[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) r[h] = *reinterpret_cast<const Raw*>(&w[h]);
+            const f2 m = Pair<IO>::cvt(__hmax2(__hmax2(r[0], r[1]), __hmax2(r[2], r[3])));
+            return fmaxf(lo(m), hi(m));
+        }
+    }
+    __device__ __forceinline__ static uint4 neg_inf() {
+        const uint32_t w = sizeof(IO) == 4                             ? 0xff800000u
+                           : std::is_same<IO, __nv_bfloat16>::value ? 0xff80ff80u
+                                                                       : 0xfc00fc00u;
+        return make_uint4(w, w, w, w);
+    }
 };
+
+// A live beam's score: finite and small enough that fp64 sums keep its logits apart.
+__device__ __forceinline__ bool beam_alive(float score) { return fabsf(score) <= kBeamMaxScore; }
 
 // The logits of one unit: `len` elements at p, the first being token v0.
 template <typename IO>
@@ -113,45 +160,53 @@ struct BeamRow {
     __device__ __forceinline__ int at(int q, int j) const { return head + q * BeamVec<IO>::E + j; }
 };
 
-// A thread's largest logit and its sum of e^{x - max}.  The difference is taken
-// before it is scaled: it cannot overflow at the type's largest values, and
-// near the maximum, where the terms that count are, it is exact.
+// A thread's largest logit and its sum of e^{x - max}, as two sums of packed
+// pairs of 2^{x log2e - r} with r = max log2e rounded; nat() takes the rounding
+// back.  Where the product could overflow (|max| above 2^64) the difference is
+// taken before it is scaled.
 struct BeamSum {
     float max = -INFINITY;
-    float base = 0.f;  // max, or 0 before any finite logit (a NaN among those still ends up in the sum)
-    float sum = 0.f;
+    float r = 0.f;  // 0 before any finite logit: a NaN among those still ends up in the sum
+    f2 sum = 0ull;
+    bool far = false;
+    // max log2e - r, the rounding of r (at most 2^-25 of it)
+    __device__ __forceinline__ float rest() const {
+        return far || max == -INFINITY ? 0.f : fmaf(max, kLog2e, -r);
+    }
     __device__ __forceinline__ void raise(float m) {
         if (m > max) {
-            sum *= ex2((max - m) * kLog2e);  // max = -inf: 0 * 0
-            max = base = m;
+            const float f = ex2((max - m) * kLog2e), e = rest();  // max = -inf: 0
+            max = m;
+            far = !(fabsf(m) < 0x1p64f);
+            r = m * kLog2e;
+            const float c = f * fmaf(rest() - e, 0.6931472f, 1.f);  // from the old rounding to the new
+            sum = mul2(sum, pk(c, c));
         }
     }
-    __device__ __forceinline__ void add(float x) { sum += ex2((x - base) * kLog2e); }
+    template <int N>
+    __device__ __forceinline__ void add(const f2 (&x)[N]) {
+        if (far) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                sum = add2(sum, pk(ex2((lo(x[i]) - max) * kLog2e), ex2((hi(x[i]) - max) * kLog2e)));
+        } else {
+            const f2 l2e = pk(kLog2e, kLog2e), nr = pk(-r, -r);
+            f2 t[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) t[i] = ex2_2(fma2(x[i], l2e, nr));
+#pragma unroll
+            for (int h = 1; h < N; h *= 2)  // a tree: no chain of additions
+#pragma unroll
+                for (int i = 0; i + h < N; i += 2 * h) t[i] = add2(t[i], t[i + h]);
+            sum = add2(sum, t[0]);
+        }
+    }
+    // the sum relative to e^max itself: 2^{r - max log2e} = 1 - rest ln 2
+    __device__ __forceinline__ float nat() const {
+        const float s = lo(sum) + hi(sum);
+        return fmaf(s, rest() * -0.6931472f, s);
+    }
 };
-
-template <typename IO>
-__device__ __forceinline__ void beam_load(const BeamRow<IO>& r, int batch, int tid, uint4 (&x)[kBeamBatch]) {
-#pragma unroll
-    for (int i = 0; i < kBeamBatch; ++i) {
-        const int q = (batch * kBeamBatch + i) * kBeamThreads + tid;
-        if (q < r.nvec) x[i] = __ldcs(reinterpret_cast<const uint4*>(r.p + r.head) + q);
-    }
-}
-
-// The pieces of one batch as floats (-inf past the end).
-template <typename IO>
-__device__ __forceinline__ void beam_unpack(const BeamRow<IO>& r, int batch, int tid,
-                                            const uint4 (&x)[kBeamBatch], float (&f)[BeamVec<IO>::N]) {
-    constexpr int E = BeamVec<IO>::E;
-#pragma unroll
-    for (int i = 0; i < kBeamBatch; ++i) {
-        const bool in = (batch * kBeamBatch + i) * kBeamThreads + tid < r.nvec;
-        IO t[E];
-        *reinterpret_cast<uint4*>(t) = x[i];
-#pragma unroll
-        for (int j = 0; j < E; ++j) f[i * E + j] = in ? Io<IO>::to_f(t[j]) : -INFINITY;
-    }
-}
 
 // A partial sum against the reference `to` (its own reference -inf: it saw no
 // finite logit, and is 0 or NaN).
@@ -159,76 +214,137 @@ __device__ __forceinline__ double beam_term(float ref, double sum, float to) {
     return ref == -INFINITY ? sum : sum * exp((double)ref - (double)to);
 }
 
-__device__ __forceinline__ void beam_push(BeamShared& s, float x, uint32_t token) {
-    const int at = atomicAdd(&s.count, 1);
-    if (at < kBeamList) s.list[at] = beam_key(x, token);
+template <typename IO>
+__device__ __forceinline__ void beam_load(const BeamRow<IO>& r, int batch, int tid, uint4 (&x)[kBeamBatch]) {
+#pragma unroll
+    for (int i = 0; i < kBeamBatch; ++i) {
+        const int q = (batch * kBeamBatch + i) * kBeamThreads + tid;
+        x[i] = q < r.nvec ? __ldcs(reinterpret_cast<const uint4*>(r.p + r.head) + q) : BeamVec<IO>::neg_inf();
+    }
+}
+
+// The n-th largest of the threads' keys (n <= 256).
+__device__ __forceinline__ uint32_t beam_bound(BeamShared& s, uint32_t key, int n) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per_warp = (n + kBeamWarps - 1) / kBeamWarps;
+    uint32_t mine = key, top = 0;
+    for (int q = 0; q < per_warp; ++q) {
+        top = __reduce_max_sync(0xffffffffu, mine);
+        const unsigned who = __ballot_sync(0xffffffffu, mine == top);
+        if (lane == __ffs(who) - 1) mine = 0;
+    }
+    if (lane == 0) s.wbound[warp] = top;
+    if (tid == 0) {
+        s.tops = 0;
+        s.count = 0;
+        s.npieces = 0;
+    }
+    __syncthreads();
+    uint32_t loose = s.wbound[0];
+#pragma unroll
+    for (int q = 1; q < kBeamWarps; ++q) loose = min(loose, s.wbound[q]);
+    // (equal keys need no order: the n-th largest value lies where those above
+    // it are fewer than n and those at or above it n or more)
+    s.top[tid] = 0;
+    __syncwarp();
+    int at = -1;
+    if (key >= loose) at = atomicAdd(&s.tops, 1);
+    __syncthreads();
+    if (at >= 0) s.top[at] = key;
+    __syncthreads();
+    if (at >= 0) {
+        const int tops = s.tops;
+        int above = 0, equal = 0;
+        const uint4* const top4 = reinterpret_cast<const uint4*>(s.top);
+#pragma unroll 4
+        for (int q = 0; q < (tops + 3) / 4; ++q) {
+            const uint4 o = top4[q];
+            above += (o.x > key) + (o.y > key) + (o.z > key) + (o.w > key);
+            equal += (o.x == key) + (o.y == key) + (o.z == key) + (o.w == key);
+        }
+        if (above < n && above + equal >= n) s.bound = key;
+    }
+    __syncthreads();
+    return s.bound;
 }
 
 // One unit: its sum and its n largest logits into `out` (the first CTA's
-// shared memory).  All threads of the CTA.
-template <typename IO>
-__device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int n, BeamUnit* out) {
-    constexpr int E = BeamVec<IO>::E, N = BeamVec<IO>::N;
+// shared memory), unless its beam is dead or finished: then its logits do not
+// count.  All threads of the CTA; `ready` is called before the first write to
+// `out`.
+template <typename IO, typename Ready>
+__device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int n, const float* score,
+                          const uint8_t* finished, BeamUnit* out, Ready ready) {
+    typedef BeamVec<IO> V;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const BeamRow<IO> row(p, len, v0);
     const int batches = (row.nvec + kBeamBatch * kBeamThreads - 1) / (kBeamBatch * kBeamThreads);
-    uint4 cur[kBeamBatch] = {}, nxt[kBeamBatch] = {};
-    beam_load(row, 0, tid, cur);
+    uint4 x0[kBeamBatch], x1[kBeamBatch], x2[kBeamBatch];
+    beam_load(row, 0, tid, x0);
     const int li = row.loose(tid);
     const float lx = li >= 0 ? Io<IO>::to_f(p[li]) : -INFINITY;
-    beam_load(row, 1, tid, nxt);
+    beam_load(row, 1, tid, x1);
+    beam_load(row, 2, tid, x2);
+    if (!beam_alive(*score) || (finished && *finished)) return;
     BeamSum sum;
-    float f[N];
-    beam_unpack(row, 0, tid, cur, f);
     float m = lx;
 #pragma unroll
-    for (int j = 0; j < N; ++j) m = fmaxf(m, f[j]);
-    // the bound: the n-th largest of the threads' first maxima
-    s.tmax[tid] = m;
-    if (tid == 0) {
-        s.count = 0;
-        s.bound = -INFINITY;
-    }
-    __syncthreads();
-    int above = 0;
-#pragma unroll 8
-    for (int q = 0; q < kBeamThreads; ++q) {
-        const float o = s.tmax[q];
-        above += o > m || (o == m && q < tid);
-    }
-    if (above == n - 1) s.bound = m;
-    __syncthreads();
-    const float bound = s.bound;
+    for (int i = 0; i < kBeamBatch; ++i) m = fmaxf(m, V::max(x0[i]));
+    const float bound = key_value((uint64_t)beam_bound(s, ordered(m), n) << 32);
+    const float most = fmaxf(bound, -3.402823466e38f);  // (-inf is no candidate)
 
     auto take = [&](float x, int at) {
-        if (x >= bound && x > -INFINITY) beam_push(s, x, v0 + (uint32_t)at);
+        if (x >= most) {
+            const int slot = atomicAdd(&s.count, 1);
+            if (slot < kBeamList) s.list[slot] = beam_key(x, v0 + (uint32_t)at);
+        }
+    };
+    auto pass = [&](const uint4 (&x)[kBeamBatch], int b) {
+        float top[kBeamBatch], most_here = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kBeamBatch; ++i) {
+            top[i] = V::max(x[i]);
+            most_here = fmaxf(most_here, top[i]);
+        }
+        sum.raise(most_here);
+#pragma unroll
+        for (int i = 0; i < kBeamBatch; ++i) {
+            f2 y[V::E / 2];
+#pragma unroll
+            for (int h = 0; h < V::E / 2; ++h) y[h] = V::pair(x[i], h);
+            sum.add(y);
+            if (top[i] >= most) {
+                const int slot = atomicAdd(&s.npieces, 1);
+                if (slot < kBeamPieces) {
+                    s.pieces()[slot] = x[i];
+                    s.piece_at[slot] = (b * kBeamBatch + i) * kBeamThreads + tid;
+                }
+            }
+        }
     };
     sum.raise(m);
-    sum.add(lx);
+    {
+        const f2 x[1] = {pk(lx, -INFINITY)};
+        sum.add(x);
+    }
     if (li >= 0) take(lx, li);
-    for (int b = 0;; ++b) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) sum.add(f[j]);
-        if (m >= bound && m > -INFINITY) {
-#pragma unroll
-            for (int j = 0; j < N; ++j) take(f[j], row.at((b * kBeamBatch + j / E) * kBeamThreads + tid, j % E));
-        }
+    for (int b = 0; b < batches; b += 3) {
+        pass(x0, b);
+        beam_load(row, b + 3, tid, x0);
         if (b + 1 >= batches) break;
-#pragma unroll
-        for (int i = 0; i < kBeamBatch; ++i) cur[i] = nxt[i];
-        beam_load(row, b + 2, tid, nxt);
-        beam_unpack(row, b + 1, tid, cur, f);
-        m = f[0];
-#pragma unroll
-        for (int j = 1; j < N; ++j) m = fmaxf(m, f[j]);
-        sum.raise(m);
+        pass(x1, b + 1);
+        beam_load(row, b + 4, tid, x1);
+        if (b + 2 >= batches) break;
+        pass(x2, b + 2);
+        beam_load(row, b + 5, tid, x2);
     }
 
-    // the unit's sum: references joined over a warp, then over the warps
+    // the unit's sum: brought to one reference over a warp, then over the warps
     float ref = sum.max;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-    double d = beam_term(sum.max, (double)sum.sum, ref);
+    // (a thread that saw no finite logit has the sum 0 or NaN)
+    double d = sum.max == -INFINITY ? sum.nat() : sum.nat() * ex2((sum.max - ref) * kLog2e);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
     if (lane == 0) {
@@ -236,24 +352,38 @@ __device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int 
         s.wsum[warp] = d;
     }
     __syncthreads();
-    const int count = s.count;
-    if (tid == 0) {
-        float r = s.wref[0];
-        for (int q = 1; q < kBeamThreads / 32; ++q) r = fmaxf(r, s.wref[q]);
-        double t = 0.0;
-        for (int q = 0; q < kBeamThreads / 32; ++q) t += beam_term(s.wref[q], s.wsum[q], r);
-        out->ref = r;
-        out->sum = t;
+    const int pieces = s.npieces;
+    for (int i = tid; i < min(pieces, kBeamPieces) * V::E; i += kBeamThreads)
+        take(Io<IO>::to_f(reinterpret_cast<const IO*>(s.pieces())[i]), row.at(s.piece_at[i / V::E], i % V::E));
+    ready();
+    __syncthreads();
+    const int count = pieces <= kBeamPieces ? s.count : kBeamList + 1;
+    if (warp == 0) {
+        const float r0 = lane < kBeamWarps ? s.wref[lane] : -INFINITY;
+        float r = r0;
+#pragma unroll
+        for (int o = kBeamWarps / 2; o > 0; o >>= 1) r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+        double t = lane < kBeamWarps ? beam_term(r0, s.wsum[lane], r) : 0.0;
+#pragma unroll
+        for (int o = kBeamWarps / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (lane == 0) {
+            out->ref = r;
+            out->sum = t;
+        }
     }
     if (count <= kBeamList) {
-        const int have = min(count, n);
         for (int i = tid; i < count; i += kBeamThreads) {
             const uint64_t key = s.list[i];
             int rank = 0;
-            for (int q = 0; q < count; ++q) rank += s.list[q] > key;
+            const ulonglong2* const list2 = reinterpret_cast<const ulonglong2*>(s.list);
+#pragma unroll 8
+            for (int q = 0; q < (count + 1) / 2; ++q) {
+                const ulonglong2 o = list2[q];
+                rank += (o.x > key) + ((2 * q + 1 < count) & (o.y > key));
+            }
             if (rank < n) out->keys[rank] = key;
         }
-        if (tid == 0) out->count = have;
+        if (tid == 0) out->count = min(count, n);
     } else {
         // one by one, each the largest key below the last
         uint64_t last = ~0ull;
@@ -272,7 +402,7 @@ __device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int 
             }
             if (lane == 0) s.wkey[warp] = best;
             __syncthreads();
-            for (int q = 0; q < kBeamThreads / 32; ++q) best = s.wkey[q] > best ? s.wkey[q] : best;
+            for (int q = 0; q < kBeamWarps; ++q) best = s.wkey[q] > best ? s.wkey[q] : best;
             __syncthreads();
             if (best == 0) break;
             if (tid == 0) out->keys[have] = best;
@@ -283,114 +413,127 @@ __device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int 
     __syncthreads();  // the shared list is free for the next unit
 }
 
-// A live beam's score: finite and small enough that fp64 sums keep its logits apart.
-__device__ __forceinline__ bool beam_alive(float score) { return fabsf(score) <= kBeamMaxScore; }
-
 // Integer order of doubles (larger first).
-__device__ __forceinline__ uint64_t ordered64(double x) {
+__device__ __forceinline__ uint64_t ordered64(double x) {  // (never 0 for a number)
     const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
     return b >> 63 ? ~b : b | 0x8000000000000000ull;
 }
 
-// Warp-wide largest of 64-bit values.
-__device__ __forceinline__ uint64_t warp_max64(uint64_t x) {
-    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(x >> 32));
-    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(x >> 32) == hi ? (uint32_t)x : 0u);
-    return ((uint64_t)hi << 32) | lo;
-}
+// A candidate of the merge: its score's integer order, and its place k V + v.
+struct alignas(16) BeamCand {
+    uint64_t key;
+    uint32_t flat;
+    float score;
+    __device__ __forceinline__ bool before(const BeamCand& o) const {
+        return (key > o.key) | ((key == o.key) & (flat < o.flat));
+    }
+};
 
 template <typename IO>
-__global__ void __launch_bounds__(kBeamThreads) wkv4_beam_select_kernel(const BeamParams p) {
+__global__ void __launch_bounds__(kBeamThreads, 3) wkv4_beam_select_kernel(const BeamParams p) {
     namespace cg = cooperative_groups;
     allow_dependents();
     grid_dependency_wait();
-    __shared__ BeamShared s;
+    extern __shared__ __align__(16) unsigned char smem[];
+    BeamShared& s = *reinterpret_cast<BeamShared*>(smem);
     cg::cluster_group cluster = cg::this_cluster();
     const int R = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-    const int64_t g = blockIdx.x / R;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t g = blockIdx.x / (unsigned)R;
     BeamShared* const first = cluster.map_shared_rank(&s, 0);
-    cluster.sync();  // every CTA of the cluster has started: its shared memory may be written
+    // every CTA of the cluster has started before its shared memory is written
+    cluster.barrier_arrive();
+    bool waited = false;
+    auto ready = [&] {
+        if (!waited) cluster.barrier_wait();
+        waited = true;
+    };
     const int units = p.K * p.S;
     for (int q = rank; q < units; q += R) {
-        const int k = q / p.S, seg = q % p.S;
+        const int k = q / p.S, seg = q - k * p.S;
         const int64_t row = g * p.K + k;
-        const float score = p.scores[row];
-        if (!beam_alive(score) || (p.finished && p.finished[row])) continue;  // no logits of this beam count
         const int64_t v0 = p.V * seg / p.S, v1 = p.V * (seg + 1) / p.S;
         beam_unit<IO>(s, static_cast<const IO*>(p.logits) + row * p.ld + v0, (int)(v1 - v0), (uint32_t)v0,
-                      p.n, &first->units[q]);
+                      p.n, p.scores + row, p.finished ? p.finished + row : nullptr, &first->units[q], ready);
     }
+    ready();
     cluster.sync();
-    if (rank != 0 || threadIdx.x >= 32) return;
+    if (rank != 0) return;
 
-    // the merge: lane q holds unit q of row k
-    const int lane = threadIdx.x, k = lane / p.S;
-    const bool mine = lane < units;
-    const float score = mine ? p.scores[g * p.K + k] : -INFINITY;
-    const bool alive = beam_alive(score);
-    const bool done = alive && p.finished && p.finished[g * p.K + k];
-    double lse = 0.0;
-    int left = 0, at = 0;  // candidates left in the unit, the next one
-    if (alive && !done) {
-        // log-sum of the row over its units
-        float ref = -INFINITY;
-        for (int q = k * p.S; q < (k + 1) * p.S; ++q) ref = fmaxf(ref, s.units[q].ref);
-        double sum = 0.0;
-        for (int q = k * p.S; q < (k + 1) * p.S; ++q)
-            sum += beam_term(s.units[q].ref, s.units[q].sum, ref);
-        lse = (double)ref + log(sum);
-        if (isfinite(lse)) left = s.units[lane].count;
-    } else if (done && lane % p.S == 0) {
-        left = 1;
+    // the rows' log-sums (NaN: no candidates)
+    if (tid < p.K) {
+        const float score = p.scores[g * p.K + tid];
+        double lse = (double)NAN;
+        if (beam_alive(score) && !(p.finished && p.finished[g * p.K + tid])) {
+            const BeamUnit* u = s.units + tid * p.S;
+            float ref = -INFINITY;
+            for (int q = 0; q < p.S; ++q) ref = fmaxf(ref, u[q].ref);
+            double sum = 0.0;
+            for (int q = 0; q < p.S; ++q) sum += beam_term(u[q].ref, u[q].sum, ref);
+            lse = (double)ref + log(sum);
+            if (!isfinite(lse)) lse = (double)NAN;
+        }
+        s.lse[tid] = lse;
     }
+    if (tid == 0) s.count = 0;
+    __syncthreads();
+    // candidates: every unit's list, or a finished beam's one
+    BeamCand* const all = reinterpret_cast<BeamCand*>(s.pieces());  // [units n], free now
+    for (int e = tid; e < units * p.n; e += kBeamThreads) {
+        const int q = e / p.n, j = e - q * p.n, k = q / p.S;
+        const float score = p.scores[g * p.K + k];
+        BeamCand c{0, 0xffffffffu, -INFINITY};
+        if (p.finished && p.finished[g * p.K + k]) {
+            if (j == 0 && q == k * p.S && beam_alive(score))
+                c = {ordered64((double)score), (uint32_t)(k * p.V) + (uint32_t)p.end_id, score};
+        } else if (s.lse[k] == s.lse[k] && j < s.units[q].count) {
+            const uint64_t key = s.units[q].keys[j];
+            const double x = (double)score + ((double)key_value(key) - s.lse[k]);
+            c = {ordered64(x), (uint32_t)(k * p.V) + ~(uint32_t)key, (float)x};
+        }
+        all[e] = c;
+    }
+    __syncthreads();
+    // at least n candidates lie at or above the least of the units' (n / units)-th best
+    const int per_unit = (p.n + units - 1) / units;
+    uint64_t loose = ~0ull;
+    for (int q = 0; q < units; ++q) loose = min(loose, all[q * p.n + per_unit - 1].key);
+    BeamCand* const some = all + units * p.n;
+    for (int e = tid; e < units * p.n; e += kBeamThreads) {
+        const BeamCand c = all[e];
+        if (c.key != 0 && c.key >= loose) some[atomicAdd(&s.count, 1)] = c;
+    }
+    __syncthreads();
+    const int count = s.count, have = min(count, p.n);
     const int64_t out = g * p.n;
-    int have = 0;
-    uint64_t next = 0;      // order of this unit's next candidate, 0: none
-    uint32_t flat = 0;
-    double val = 0.0;
-    auto fetch = [&] {
-        next = 0;
-        if (left > 0) {
-            uint32_t token = (uint32_t)p.end_id;
-            val = (double)score;
-            if (!done) {
-                const uint64_t key = s.units[lane].keys[at];
-                token = ~(uint32_t)key;
-                val = (double)score + ((double)key_value(key) - lse);
-            }
-            flat = (uint32_t)(k * p.V) + token;
-            next = ordered64(val);
-            ++at;
-            --left;
+    for (int e = tid; e < count; e += kBeamThreads) {
+        const BeamCand c = some[e];
+        int above = 0;
+#pragma unroll 8
+        for (int q = 0; q < count; ++q) above += some[q].before(c);
+        if (above < p.n) {
+            const uint32_t k = c.flat / (uint32_t)p.V;
+            p.out_scores[out + above] = c.score;
+            p.out_parents[out + above] = (int32_t)k;
+            p.out_tokens[out + above] = (int32_t)(c.flat - k * (uint32_t)p.V);
+            s.best[above] = c.flat;
         }
-    };
-    fetch();
-    for (; have < p.n; ++have) {
-        const uint64_t top = warp_max64(next);
-        if (top == 0) break;
-        const uint32_t lowest = __reduce_min_sync(0xffffffffu, next == top ? flat : 0xffffffffu);
-        if (next == top && flat == lowest) {
-            p.out_scores[out + have] = (float)val;
-            p.out_parents[out + have] = k;
-            p.out_tokens[out + have] = (int32_t)(flat - (uint32_t)(k * p.V));
-            s.best[have] = flat;
-            fetch();
-        }
-        __syncwarp();
     }
+    if (have == p.n) return;
     // fewer candidates than n: the lowest entries not taken, at -inf
-    for (uint32_t f = 0; have < p.n; ++f) {
+    __syncthreads();
+    if (tid >= 32) return;
+    int filled = have;
+    for (uint32_t f = 0; filled < p.n; ++f) {
         bool taken = false;
         for (int i = lane; i < have; i += 32) taken |= s.best[i] == f;
         if (__any_sync(0xffffffffu, taken)) continue;
         if (lane == 0) {
-            p.out_scores[out + have] = -INFINITY;
-            p.out_parents[out + have] = (int32_t)(f / (uint32_t)p.V);
-            p.out_tokens[out + have] = (int32_t)(f % (uint32_t)p.V);
-            s.best[have] = f;
+            p.out_scores[out + filled] = -INFINITY;
+            p.out_parents[out + filled] = (int32_t)(f / (uint32_t)p.V);
+            p.out_tokens[out + filled] = (int32_t)(f % (uint32_t)p.V);
         }
-        __syncwarp();
-        ++have;
+        ++filled;
     }
 }
 

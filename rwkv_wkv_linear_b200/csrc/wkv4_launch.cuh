@@ -16,21 +16,26 @@
 
 namespace wkv4 {
 
-// The dynamic shared memory limit is a per-device function attribute: set it
-// once per device for each kernel instantiation.
+// A function attribute (the dynamic shared memory limit, say) is one per
+// device: set once per device for each kernel instantiation.
 struct DeviceFlags {
     std::atomic<bool> done[64];
 };
 
 template <typename Kern>
-inline cudaError_t ensure_smem_attr(DeviceFlags& f, Kern kern, size_t smem) {
+inline cudaError_t ensure_attr(DeviceFlags& f, Kern kern, cudaFuncAttribute attr, int value) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64 && f.done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(kern, attr, value);
     if (e == cudaSuccess && dev >= 0 && dev < 64) f.done[dev].store(true, std::memory_order_release);
     return e;
+}
+
+template <typename Kern>
+inline cudaError_t ensure_smem_attr(DeviceFlags& f, Kern kern, size_t smem) {
+    return ensure_attr(f, kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
 inline int env_int(const char* name, int dflt) {
