@@ -169,7 +169,7 @@ cudaError_t launch_backward(const BwdArgs& a) {
 // ------------------------------------------------------------- token shift
 
 // Runs of the token shift's backward pass: as many CTAs as the GPU holds at
-// once (8 of 128 threads an SM), at least kShiftMinRun steps a run.
+// once, at least kShiftMinRun steps a run.
 struct ShiftBwdShape {
     int V;
     int64_t run, yblocks;
@@ -179,7 +179,7 @@ static ShiftBwdShape shift_bwd_shape(int64_t B, int64_t T, int64_t C, bool vec) 
     ShiftBwdShape s;
     s.V = vec ? 4 : 1;
     const int64_t xb = (C + kShiftBwdX * s.V - 1) / (kShiftBwdX * s.V);
-    const int64_t blocks = std::max<int64_t>(1, (int64_t)148 * 8 / std::max<int64_t>(1, xb * B));
+    const int64_t blocks = std::max<int64_t>(1, (int64_t)148 * kShiftBwdCtas / std::max<int64_t>(1, xb * B));
     const int64_t runs = blocks * kShiftBwdY;
     s.run = std::max<int64_t>((T + runs - 1) / runs, kShiftMinRun);
     s.run = std::max<int64_t>(s.run, (T + 65535ll * kShiftBwdY - 1) / (65535ll * kShiftBwdY));
