@@ -16,7 +16,8 @@
 //   gw   = sum_t e^w (P_{t+1} A_t + Q_{t+1} D_t).
 // So there are two scans, one from each end, and the second needs the first.
 //
-// Layout.  A tile is 64 channels of one batch row; a warp owns L = 16 steps
+// Layout.  A tile is 64 channels of one batch row; a warp owns L steps (32, or
+// 16 in fp32 while T fits one round)
 // of it, a lane two adjacent channels (packed f32x2 arithmetic), a CTA NW
 // warps, a cluster of NC CTAs a round of NC NW L steps.  A round's k, v, gout
 // (and r) are copied to shared memory once and stay there:
@@ -63,8 +64,6 @@
 
 namespace wkv4 {
 
-// steps a warp chunk (a warp's rows are L steps x 64 channels)
-template <typename IO> constexpr int kBwdL = sizeof(IO) == 2 ? 32 : 16;
 constexpr int kBwdC = 64;   // channels a tile
 constexpr int kBwdWarps = 4;    // warps a CTA
 constexpr int kBwdMaxCtas = 8;  // CTAs a cluster
@@ -103,9 +102,8 @@ struct BwdParams {
 // r) as loaded, then the warps' chunk sums [NW], the other CTAs' sums
 // [kBwdMaxCtas] and the sum after a round [2], four barriers and the
 // tensor-memory base.
-template <typename IO, bool kGate>
+template <typename IO, int L, bool kGate>
 struct BwdLayout {
-    static constexpr int L = kBwdL<IO>;
     static constexpr int kTile = L * kBwdC * (int)sizeof(IO);  // one tensor's rows of a warp
     static constexpr int kWarp = (kGate ? 4 : 3) * kTile;
     static constexpr int kChunks = kBwdWarps * kWarp;
@@ -250,45 +248,57 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A warp's n rows of 64 channels from c0 of a [B][T][C] tensor (src: the first
-// row, channel 0) into shared memory; channels past C read as zero, rows past
-// n are left.  vec: every row starts on 16 bytes, 16-byte asynchronous copies;
-// otherwise element by element.
-template <typename IO>
-__device__ __forceinline__ void load_rows(unsigned char* dst, const IO* src, int64_t C, int c0, int n,
-                                          int lane, bool vec) {
+// A warp's n rows of 64 channels from c0 of N [B][T][C] tensors (src: the first
+// row, channel 0) into shared memory, L rows a tensor one after another;
+// channels past C read as zero, rows past n are left.  vec: every row starts
+// on 16 bytes, 16-byte asynchronous copies; otherwise element by element, 8
+// rows of every tensor in flight.
+template <typename IO, int L, int N>
+__device__ __forceinline__ void load_rows(unsigned char* dst, const IO* const (&src)[N], int64_t C, int c0,
+                                          int n, int lane, bool vec) {
     constexpr int kE = 16 / (int)sizeof(IO), kP = kBwdC / kE;  // elements a piece, pieces a row
+    constexpr int kTile = L * kBwdC * (int)sizeof(IO);
     if (vec) {
         constexpr int kR = 32 / kP;  // rows a pass of the warp
         const int row = lane / kP, piece = lane % kP;
         const int c = c0 + piece * kE;
         const int bytes = c < C ? 16 : 0;
         const uint32_t d = smem_u32(dst) + (uint32_t)(row * kBwdC * (int)sizeof(IO) + piece * 16);
-        const IO* s = src + (int64_t)row * C + (c < C ? c : 0);
+        const int64_t o = (int64_t)row * C + (c < C ? c : 0);
 #pragma unroll
-        for (int q = 0; q < kBwdL<IO> / kR; ++q) {
-            if (q * kR + row < n) cp_async16(d + (uint32_t)(q * kR * kBwdC * (int)sizeof(IO)), s, bytes);
-            s += (int64_t)kR * C;
+        for (int h = 0; h < N; ++h) {
+            const IO* s = src[h] + o;
+#pragma unroll
+            for (int q = 0; q < L / kR; ++q) {
+                if (q * kR + row < n)
+                    cp_async16(d + (uint32_t)(h * kTile + q * kR * kBwdC * (int)sizeof(IO)), s, bytes);
+                s += (int64_t)kR * C;
+            }
         }
     } else {
         IO* d = reinterpret_cast<IO*>(dst) + lane;
-        const IO* s = src + c0 + lane;
         const bool ok0 = c0 + lane < C, ok1 = c0 + lane + 32 < C;
-        constexpr int kG = 8;  // rows in flight
+        int64_t o = c0 + lane;
+        constexpr int kG = 8;
 #pragma unroll 1
         for (int q = 0; q < n; q += kG) {
-            IO x[kG][2];
+            IO x[N][kG][2];
 #pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                x[i][0] = ok0 && q + i < n ? s[(int64_t)i * C] : Io<IO>::from_f(0.f);
-                x[i][1] = ok1 && q + i < n ? s[(int64_t)i * C + 32] : Io<IO>::from_f(0.f);
-            }
+            for (int h = 0; h < N; ++h)
 #pragma unroll
-            for (int i = 0; i < kG; ++i) {
-                d[(q + i) * kBwdC] = x[i][0];
-                d[(q + i) * kBwdC + 32] = x[i][1];
-            }
-            s += (int64_t)kG * C;
+                for (int i = 0; i < kG; ++i) {
+                    const IO* s = src[h] + o + (int64_t)i * C;
+                    x[h][i][0] = ok0 && q + i < n ? s[0] : Io<IO>::from_f(0.f);
+                    x[h][i][1] = ok1 && q + i < n ? s[32] : Io<IO>::from_f(0.f);
+                }
+#pragma unroll
+            for (int h = 0; h < N; ++h)
+#pragma unroll
+                for (int i = 0; i < kG; ++i) {
+                    d[(h * L + q + i) * kBwdC] = x[h][i][0];
+                    d[(h * L + q + i) * kBwdC + 32] = x[h][i][1];
+                }
+            o += (int64_t)kG * C;
         }
     }
 }
@@ -535,14 +545,14 @@ constexpr int kUpShift = 40;
 
 // Step 3.  kPlain: a whole chunk with every lane's two channels present, on the
 // fixed-reference path and stored as pairs.
-template <typename IO, bool kGate, bool kPlain>
+template <typename IO, int L, bool kGate, bool kPlain>
 __device__ __forceinline__ void bwd_walk_up(const BwdChunk<IO>& ch, const BwdConsts& cc, f2 nref, f2 A,
                                             f2 D, IO* gr, int64_t C, bool vec, bool s0, bool s1, BwdUp& o) {
     const f2 l2e = pk(kLog2e, kLog2e), one = pk(1.f, 1.f), m1 = pk(-1.f, -1.f);
     f2 Ap = 0ull, Dp = 0ull, gw = 0ull, gu = 0ull, P = 0ull, Q = 0ull;
     f2 f = pk(0x1p40f, 0x1p40f);
 #pragma unroll 1
-    for (int q = 0; q < (kPlain ? kBwdL<IO> : ch.n); q += 4) {
+    for (int q = 0; q < (kPlain ? L : ch.n); q += 4) {
         uint32_t st[16];
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
@@ -595,11 +605,11 @@ __device__ __forceinline__ void bwd_walk_up(const BwdChunk<IO>& ch, const BwdCon
 
 // Step 5: gk, gv from (P, Q) at the chunk's end; (P, Q) at its start in P, Q.
 // With h = e^u al + P and j = -e^u al y + Q: gv = e h, gk = e (h v + j).
-template <typename IO, bool kPlain>
+template <typename IO, int L, bool kPlain>
 __device__ __forceinline__ void bwd_walk_down(const BwdChunk<IO>& ch, const BwdConsts& cc, f2 nref, f2& P,
                                               f2& Q, IO* gk, IO* gv, int64_t C, bool vec, bool s0, bool s1) {
     const f2 l2e = pk(kLog2e, kLog2e);
-    const int n = kPlain ? kBwdL<IO> : ch.n;
+    const int n = kPlain ? L : ch.n;
 #pragma unroll 1
     for (int q = (n - 1) & ~7; q >= 0; q -= 8) {
         uint32_t st[32];
@@ -628,13 +638,13 @@ __device__ __forceinline__ void bwd_walk_down(const BwdChunk<IO>& ch, const BwdC
     }
 }
 
-template <typename IO, bool kGate>
+template <typename IO, int L, bool kGate>
 __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const BwdParams p) {
     namespace cg = cooperative_groups;
     allow_dependents();
     grid_dependency_wait();
-    using Lay = BwdLayout<IO, kGate>;
-    constexpr int NW = kBwdWarps, L = kBwdL<IO>, Ts = NW * L;  // steps of a chunk, of a CTA in a round
+    using Lay = BwdLayout<IO, L, kGate>;
+    constexpr int NW = kBwdWarps, Ts = NW * L;  // steps of a chunk, of a CTA in a round
     constexpr int P = NW / 2;              // threads that join a channel's chunks, two chunks each
     constexpr unsigned kAll = 0xffffffffu;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -671,12 +681,15 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         const int t0 = round * round_steps + rank * Ts + warp * L;
         const int n = chunk_steps(T, t0, L);
         const int64_t at = ((int64_t)b * T + t0) * C;
-        const void* const src[4] = {p.k, p.v, p.gy, p.r};
-#pragma unroll
-        for (int q = 0; q < (kGate ? 4 : 3); ++q) {
-            load_rows<IO>(wbase + q * Lay::kTile, static_cast<const IO*>(src[q]) + at, C, c0, n, lane,
-                          p.vec_load);
-            if (q == 1) cp_async_commit();
+        const IO* const kv[2] = {static_cast<const IO*>(p.k) + at, static_cast<const IO*>(p.v) + at};
+        load_rows<IO, L>(wbase, kv, C, c0, n, lane, p.vec_load);
+        cp_async_commit();
+        if constexpr (kGate) {
+            const IO* const gr[2] = {static_cast<const IO*>(p.gy) + at, static_cast<const IO*>(p.r) + at};
+            load_rows<IO, L>(wbase + 2 * Lay::kTile, gr, C, c0, n, lane, p.vec_load);
+        } else {
+            const IO* const g[1] = {static_cast<const IO*>(p.gy) + at};
+            load_rows<IO, L>(wbase + 2 * Lay::kTile, g, C, c0, n, lane, p.vec_load);
         }
         cp_async_commit();
     };
@@ -818,10 +831,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         BwdUp up;
         const bool plain = __all_sync(kAll, n == L && p.vec_store && ok1 && fast[0] && fast[1]);
         if (plain) {
-            bwd_walk_up<IO, kGate, true>(ch, cc, nref, pk(a0[0], a0[1]), pk(b0[0], b0[1]), gr, C, true, true,
+            bwd_walk_up<IO, L, kGate, true>(ch, cc, nref, pk(a0[0], a0[1]), pk(b0[0], b0[1]), gr, C, true, true,
                                          true, up);
         } else {
-            bwd_walk_up<IO, kGate, false>(ch, cc, nref, pk(a0[0], a0[1]), pk(b0[0], b0[1]), gr, C,
+            bwd_walk_up<IO, L, kGate, false>(ch, cc, nref, pk(a0[0], a0[1]), pk(b0[0], b0[1]), gr, C,
                                           p.vec_store, ok0 && fast[0], ok1 && fast[1], up);
         }
         auto exact_chunk = [&](int j) {
@@ -918,9 +931,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         IO* const gk = static_cast<IO*>(p.gk) + at + c;
         IO* const gv = static_cast<IO*>(p.gv) + at + c;
         if (plain && __all_sync(kAll, fastR[0] && fastR[1])) {
-            bwd_walk_down<IO, true>(ch, cc, nref, Pw, Qw, gk, gv, C, true, true, true);
+            bwd_walk_down<IO, L, true>(ch, cc, nref, Pw, Qw, gk, gv, C, true, true, true);
         } else {
-            bwd_walk_down<IO, false>(ch, cc, nref, Pw, Qw, gk, gv, C, p.vec_store, ok0 && fastR[0],
+            bwd_walk_down<IO, L, false>(ch, cc, nref, Pw, Qw, gk, gv, C, p.vec_store, ok0 && fastR[0],
                                      ok1 && fastR[1]);
         }
         float gwj[2] = {lo(gw), hi(gw)}, guj[2] = {lo(up.gu), hi(up.gu)};
@@ -983,11 +996,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
 
 // Summary of every round's k, v (several rounds): CTA (tile, round), each
 // warp walking its NC chunks of L steps with the next chunk's rows in flight.
-template <typename IO>
+template <typename IO, int L>
 __global__ void __launch_bounds__(32 * kBwdWarps) wkv4_backward_summary_kernel(const BwdParams p, int NC) {
     allow_dependents();
     grid_dependency_wait();
-    constexpr int NW = kBwdWarps, L = kBwdL<IO>, kTile = BwdLayout<IO, false>::kTile;
+    constexpr int NW = kBwdWarps, kTile = BwdLayout<IO, L, false>::kTile;
     extern __shared__ __align__(16) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 2 * lane;
     const int round = blockIdx.y, b = blockIdx.z, c0 = (int)blockIdx.x * kBwdC, T = (int)p.T;
@@ -1002,8 +1015,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps) wkv4_backward_summary_kernel(c
         const int n = q < NC ? chunk_steps(T, t, L) : 0;
         unsigned char* const d = buf + (q & 1) * 2 * kTile;
         const int64_t at = ((int64_t)b * T + t) * C;
-        load_rows<IO>(d, static_cast<const IO*>(p.k) + at, C, c0, n, lane, p.vec_load);
-        load_rows<IO>(d + kTile, static_cast<const IO*>(p.v) + at, C, c0, n, lane, p.vec_load);
+        const IO* const kv[2] = {static_cast<const IO*>(p.k) + at, static_cast<const IO*>(p.v) + at};
+        load_rows<IO, L>(d, kv, C, c0, n, lane, p.vec_load);
         cp_async_commit();
     };
     const Decay dL[2] = {decay_of(rate_of(cc.w[0]), L), decay_of(rate_of(cc.w[1]), L)};

@@ -15,18 +15,26 @@ namespace wkv4 {
 // Launch shape of the backward pass, from the sizes and the type alone (the
 // workspace is sized from it): CTAs a cluster, batch rows a cluster, rounds.
 struct BwdShape {
-    int NC, nb;
+    int L, NC, nb;
     int64_t rounds;
     int64_t rows(int64_t B) const { return (B + nb - 1) / nb * NC; }  // partial sums a channel
 };
 
-static BwdShape bwd_shape(int64_t B, int64_t T, int64_t C, int dtype) {
+static BwdShape bwd_shape(int64_t B, int64_t T, int64_t C, int dtype, bool gated) {
     BwdShape s;
-    const int64_t steps = kBwdWarps * (dtype == WKV4_F32 ? kBwdL<float> : kBwdL<__half>);
-    const int64_t ctas = std::max<int64_t>(1, (T + steps - 1) / steps);
-    s.NC = 1;
-    while (s.NC < 8 && s.NC < ctas) s.NC *= 2;
-    s.rounds = (ctas + s.NC - 1) / s.NC;
+    const int64_t tiles = (C + kBwdC - 1) / kBwdC * B;
+    auto shape = [&](int L) {
+        const int64_t ctas = std::max<int64_t>(1, (T + kBwdWarps * L - 1) / (kBwdWarps * L));
+        s.L = L;
+        s.NC = 1;
+        while (s.NC < kBwdMaxCtas && s.NC < ctas) s.NC *= 2;
+        s.rounds = (ctas + s.NC - 1) / s.NC;
+    };
+    // Steps a chunk: 32; in fp32 (twice the shared memory, so fewer CTAs an SM)
+    // 16 unless the CTAs are few and walk several rounds, whose joins are then
+    // spread over twice the steps (B=1, T=16384, C=2048: 322 -> 248 us).
+    shape(dtype == WKV4_F32 ? 16 : 32);
+    if (dtype == WKV4_F32 && !gated && s.rounds > 1 && tiles * s.NC <= 2 * 148) shape(32);
     // Batch rows a cluster walks one after another, its set-up (constants,
     // barriers, tensor memory) paid once for all of them: the most, up to 4,
     // that do not lengthen the waves of CTAs (3 an SM) times the rows each
@@ -53,8 +61,12 @@ static size_t bwd_part_bytes(int64_t B, int64_t C, const BwdShape& s) {
 }
 
 size_t backward_workspace(int64_t B, int64_t T, int64_t C, int dtype) {
-    const BwdShape s = bwd_shape(B, T, C, dtype);
-    return bwd_part_bytes(B, C, s) + (s.rounds > 1 ? (size_t)s.rounds * B * C * kSumBytes : 0);
+    size_t most = 0;  // gated or not
+    for (bool gated : {false, true}) {
+        const BwdShape s = bwd_shape(B, T, C, dtype, gated);
+        most = std::max(most, bwd_part_bytes(B, C, s) + (s.rounds > 1 ? (size_t)s.rounds * B * C * kSumBytes : 0));
+    }
+    return most;
 }
 
 static cudaError_t launch_column_sum(const float* part, float* o0, float* o1, float* o2, int n,
@@ -64,16 +76,16 @@ static cudaError_t launch_column_sum(const float* part, float* o0, float* o1, fl
                       dim3(256), 0, stream, p);
 }
 
-template <typename IO, bool kGate>
+template <typename IO, int L, bool kGate>
 static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdShape& sh) {
-    using Lay = BwdLayout<IO, kGate>;
-    auto kern = wkv4_backward_kernel<IO, kGate>;
+    using Lay = BwdLayout<IO, L, kGate>;
+    auto kern = wkv4_backward_kernel<IO, L, kGate>;
     static DeviceFlags attr;
     cudaError_t e = ensure_smem_attr(attr, kern, Lay::kBytes);
     if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)((a.C + kBwdC - 1) / kBwdC), threads = 32 * kBwdWarps;
     if (sh.rounds > 1) {
-        auto sum = wkv4_backward_summary_kernel<IO>;
+        auto sum = wkv4_backward_summary_kernel<IO, L>;
         const size_t smem = kBwdWarps * (4 * Lay::kTile + kBwdC * kSumBytes);
         static DeviceFlags sattr;
         e = ensure_smem_attr(sattr, sum, smem);
@@ -83,7 +95,7 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
         if (e != cudaSuccess) return e;
         const int64_t BC = a.B * a.C;
         e = launch_pdl(wkv4_backward_prefix_kernel, launch_grid(dim3((unsigned)((BC + 127) / 128))),
-                       dim3(128), 0, a.stream, p, (int64_t)sh.NC * kBwdWarps * kBwdL<IO>);
+                       dim3(128), 0, a.stream, p, (int64_t)sh.NC * kBwdWarps * L);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg;
@@ -110,11 +122,16 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
 
 template <typename IO>
 static cudaError_t launch_backward_io(const BwdArgs& a, BwdParams& p, const BwdShape& sh) {
-    return a.r ? launch_backward_t<IO, true>(a, p, sh) : launch_backward_t<IO, false>(a, p, sh);
+    if constexpr (sizeof(IO) == 4) {
+        if (sh.L == 32) return launch_backward_t<IO, 32, false>(a, p, sh);
+        return a.r ? launch_backward_t<IO, 16, true>(a, p, sh) : launch_backward_t<IO, 16, false>(a, p, sh);
+    } else {
+        return a.r ? launch_backward_t<IO, 32, true>(a, p, sh) : launch_backward_t<IO, 32, false>(a, p, sh);
+    }
 }
 
 cudaError_t launch_backward(const BwdArgs& a) {
-    const BwdShape sh = bwd_shape(a.B, a.T, a.C, a.dtype);
+    const BwdShape sh = bwd_shape(a.B, a.T, a.C, a.dtype, a.r != nullptr);
     BwdParams p{};
     p.B = a.B;
     p.T = a.T;
