@@ -151,7 +151,9 @@ __device__ __forceinline__ Rate rate_of(float w) {
 __device__ __forceinline__ Decay decay_of(Rate r, int n) {
     const float x = (float)n * r.hi;
     const float c = ceilf(x);
-    return {ex2((x - c) + (fmaf((float)n, r.hi, -x) + (float)n * r.lo)), (int)c};
+    // (exp2f, not ex2.approx: the factor is applied once a chunk, and its error
+    // grows with the number of chunks a slow decay remembers)
+    return {exp2f((x - c) + (fmaf((float)n, r.hi, -x) + (float)n * r.lo)), (int)c};
 }
 __device__ __forceinline__ Sum decayed(Sum x, Decay d) { return {x.a * d.f, x.b * d.f, x.p + d.i}; }
 // a 2^p, b 2^p with a fractional p
@@ -437,13 +439,16 @@ constexpr f2 kSigns = 0x8000000080000000ull;
 struct BwdConsts {
     f2 ew, eu;
     float w[2], u[2];
+    // e^w to half a step of its fp32 value: near 1, where it is applied many
+    // times over, 1 + (e^w - 1) is rounded once
+    __device__ __forceinline__ static float decay(float w) { return fabsf(w) < 0.5f ? 1.f + expm1f(w) : expf(w); }
     __device__ __forceinline__ BwdConsts(const float* gw, const float* gu, int64_t c, int64_t C) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             w[j] = c + j < C ? __ldg(gw + c + j) : 0.f;
             u[j] = c + j < C ? __ldg(gu + c + j) : 0.f;
         }
-        ew = pk(expf(w[0]), expf(w[1]));
+        ew = pk(decay(w[0]), decay(w[1]));
         eu = pk(expf(u[0]), expf(u[1]));
     }
 };

@@ -53,13 +53,13 @@ cudaError_t launch_beam_select(const BeamArgs& a) {
     p.out_scores = a.out_scores;
     p.out_parents = a.out_parents;
     p.out_tokens = a.out_tokens;
-    // a CTA a 2048 logits of the group or more, at most 8 a cluster -- 16 (which
-    // an SM cluster of the GPU may not have room for twice) while the groups
-    // leave SMs idle otherwise: one request of 4 beams 9.6 us against 10.6,
-    // 48 requests of 8 beams 41.2 us against 25.7 with 8.
+    // CTAs a group: one a beam or one a 2048 logits, whichever are more, at most
+    // 8 a cluster -- 16 (which a group of SMs may not have room for twice) while
+    // the groups leave SMs idle otherwise: one request of 4 beams 9.3 us against
+    // 10.6, 48 requests of 8 beams 41.2 us against 25.7 with 8.
     const int most = a.G * 16 <= 148 ? 16 : 8;
     int R = 1;
-    while (R < most && a.K * a.V >= 2 * R * 2048) R *= 2;
+    while (R < most && (R < a.K || a.K * a.V >= 2 * R * 2048)) R *= 2;
     p.S = 1;
     while (p.S * 2 * a.K <= R) p.S *= 2;
     switch (a.dtype) {

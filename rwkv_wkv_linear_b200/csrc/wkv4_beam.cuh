@@ -208,10 +208,21 @@ struct BeamSum {
     }
 };
 
+// log x for x >= 1/2 to about 2^-24: the exponent in fp64, log of the mantissa in
+// [0.7, 1.4] in fp32 with what its rounding left out.
+__device__ __forceinline__ double beam_log(double x) {
+    if (!(x >= 0.5 && x < 1e300)) return log(x);
+    const long long bits = __double_as_longlong(x) - 0x3fe6a09e667f3bcdll;  // of sqrt(1/2)
+    const int e = (int)(bits >> 52);
+    const double m = __longlong_as_double(__double_as_longlong(x) - ((long long)e << 52));
+    const float f = (float)m;
+    return (double)e * kLn2D + (double)(logf(f) + (float)(m - (double)f) / f);
+}
+
 // A partial sum against the reference `to` (its own reference -inf: it saw no
 // finite logit, and is 0 or NaN).
 __device__ __forceinline__ double beam_term(float ref, double sum, float to) {
-    return ref == -INFINITY ? sum : sum * exp((double)ref - (double)to);
+    return ref == -INFINITY ? sum : sum * (double)expf(ref - to);
 }
 
 template <typename IO>
@@ -470,7 +481,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) wkv4_beam_select_kernel(const
             for (int q = 0; q < p.S; ++q) ref = fmaxf(ref, u[q].ref);
             double sum = 0.0;
             for (int q = 0; q < p.S; ++q) sum += beam_term(u[q].ref, u[q].sum, ref);
-            lse = (double)ref + log(sum);
+            lse = (double)ref + beam_log(sum);
             if (!isfinite(lse)) lse = (double)NAN;
         }
         s.lse[tid] = lse;

@@ -7,6 +7,7 @@ library cannot be loaded every call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -46,6 +47,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libwkv4.so (raises OSError when it is missing: build it with
     ``python -m rwkv_wkv_linear_b200._build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -445,6 +448,57 @@ def state_combine(x: Optional[torch.Tensor], y: torch.Tensor, n_steps: int, w: t
     return out
 
 
+# The calls below are short beside a kernel of a few microseconds, so their host
+# side is kept lean: one pass over the arguments, plain integers for addresses,
+# no device switch when the device is already current.
+
+_HERE = contextlib.nullcontext()
+# the current stream's handle without building a torch.cuda.Stream (2 us); torch's
+# own compiler asks for it the same way
+_current_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _on(dev: torch.device):
+    """Makes `dev` current (nothing to do when it is)."""
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _require(dev: torch.device, dtype: torch.dtype, **tensors):
+    """The given tensors (None entries skipped) are contiguous, of `dtype` and on `dev`."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, other arguments on {dev}" if t.is_cuda
+                             else f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _shape(shape, what: str, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {what}")
+
+
+def _cuda(name: str, t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def _adr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, dev: torch.device) -> int:
+    if stream is None and _current_raw is not None:
+        return _current_raw(dev.index)
+    return _stream(stream, dev).value or 0
+
+
 class Grads(NamedTuple):
     """Gradients of a forward call (gr: gated only; gstate_in: with a state_in only)."""
     gk: torch.Tensor
@@ -468,9 +522,7 @@ def _workspace(given: Optional[torch.Tensor], need: int, dev: torch.device, stre
     """The call's workspace: the caller's, or a new one.  A new one is dropped
     when the call returns, so the allocator is told which stream still uses it."""
     if given is not None:
-        if given.dtype != torch.uint8:
-            raise ValueError("workspace must be uint8")
-        _check_dev("workspace", given)
+        _require(dev, torch.uint8, workspace=given)
         return given
     if need == 0:
         return None
@@ -493,36 +545,32 @@ def backward(k: torch.Tensor, v: torch.Tensor, w: torch.Tensor, u: torch.Tensor,
     r, gy [B, T, C] of one dtype; w, u [C] fp32; states [3, B, C] fp32.
     workspace: CUDA uint8, at least backward_workspace_bytes(...) (allocated
     when None)."""
-    if k.dim() != 3 or v.shape != k.shape or gy.shape != k.shape or (r is not None and r.shape != k.shape):
+    if k.dim() != 3:
         raise ValueError("k, v, gy (and r) must all be [B, T, C]")
     B, T, C = k.shape
     dt = _DTYPES.get(k.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {k.dtype}")
-    for name, t in (("k", k), ("v", v), ("gy", gy), ("r", r)):
-        _check_dev(name, t, k.dtype)
-    for name, t in (("w", w), ("u", u)):
-        _check_dev(name, t, torch.float32)
-        if t.shape != (C,):
-            raise ValueError(f"{name} must be [C]")
-    for name, t in (("state_in", state_in), ("state_out", state_out), ("gstate_out", gstate_out)):
-        _check_dev(name, t, torch.float32)
-        if t is not None and t.shape != (3, B, C):
-            raise ValueError(f"{name} must be [3, B, C]")
+    dev = _cuda("k", k)
+    _require(dev, k.dtype, k=k, v=v, gy=gy, r=r)
+    _require(dev, torch.float32, w=w, u=u, state_in=state_in, state_out=state_out, gstate_out=gstate_out)
+    _shape(k.shape, "[B, T, C]", v=v, gy=gy, r=r)
+    _shape((C,), "[C]", w=w, u=u)
+    _shape((3, B, C), "[3, B, C]", state_in=state_in, state_out=state_out, gstate_out=gstate_out)
     if gstate_out is not None and state_out is None:
         raise ValueError("gstate_out needs the state_out it is the gradient of")
-    dev = _one_device(k=k, v=v, w=w, u=u, gy=gy, r=r, state_in=state_in, state_out=state_out,
-                      gstate_out=gstate_out, workspace=workspace)
-    with torch.cuda.device(dev):
+    lib = load()
+    with _on(dev):
         gk, gv = torch.empty_like(k), torch.empty_like(v)
         gr = torch.empty_like(r) if r is not None else None
         gw, gu = torch.empty_like(w), torch.empty_like(u)
         gs = torch.empty_like(state_in) if state_in is not None else None
-        ws = _workspace(workspace, load().wkv4_backward_workspace(B, T, C, dt), dev, stream)
-        rc = load().wkv4_backward(B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r),
-                                  _ptr(state_in), _ptr(gy), _ptr(state_out), _ptr(gstate_out),
-                                  _ptr(gk), _ptr(gv), _ptr(gr), _ptr(gw), _ptr(gu), _ptr(gs),
-                                  _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream, dev), dt)
+        ws = _workspace(workspace, lib.wkv4_backward_workspace(B, T, C, dt), dev, stream)
+        rc = lib.wkv4_backward(B, T, C, w.data_ptr(), u.data_ptr(), k.data_ptr(), v.data_ptr(), _adr(r),
+                               _adr(state_in), gy.data_ptr(), _adr(state_out), _adr(gstate_out),
+                               gk.data_ptr(), gv.data_ptr(), _adr(gr), gw.data_ptr(), gu.data_ptr(),
+                               _adr(gs), _adr(ws), 0 if ws is None else ws.numel(),
+                               _raw_stream(stream, dev), dt)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_backward")
     return Grads(gk, gv, gr, gw, gu, gs)
@@ -551,32 +599,25 @@ def token_shift_backward(x: torch.Tensor, mix_k: torch.Tensor, mix_v: torch.Tens
     dt = _DTYPES.get(x.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
-    for name, t in (("x", x), ("gxk", gxk), ("gxv", gxv), ("gxr", gxr)):
-        _check_dev(name, t, x.dtype)
-        if t is not None and t.shape != x.shape:
-            raise ValueError(f"{name} must be [B, T, C]")
-    for name, m in (("mix_k", mix_k), ("mix_v", mix_v), ("mix_r", mix_r)):
-        _check_dev(name, m, torch.float32)
-        if m is not None and m.shape != (C,):
-            raise ValueError(f"{name} must be [C]")
-    for name, t in (("x_prev", x_prev), ("gx_last", gx_last)):
-        _check_dev(name, t, x.dtype)
-        if t is not None and t.shape != (B, C):
-            raise ValueError(f"{name} must be [B, C]")
-    dev = _one_device(x=x, mix_k=mix_k, mix_v=mix_v, mix_r=mix_r, gxk=gxk, gxv=gxv, gxr=gxr,
-                      x_prev=x_prev, gx_last=gx_last, workspace=workspace)
-    with torch.cuda.device(dev):
+    dev = _cuda("x", x)
+    _require(dev, x.dtype, x=x, gxk=gxk, gxv=gxv, gxr=gxr, x_prev=x_prev, gx_last=gx_last)
+    _require(dev, torch.float32, mix_k=mix_k, mix_v=mix_v, mix_r=mix_r)
+    _shape(x.shape, "[B, T, C]", gxk=gxk, gxv=gxv, gxr=gxr)
+    _shape((C,), "[C]", mix_k=mix_k, mix_v=mix_v, mix_r=mix_r)
+    _shape((B, C), "[B, C]", x_prev=x_prev, gx_last=gx_last)
+    lib = load()
+    with _on(dev):
         gx = torch.empty_like(x)
         gp = torch.empty_like(x_prev) if x_prev is not None else None
         gk, gv = torch.empty_like(mix_k), torch.empty_like(mix_v)
         gr = torch.empty_like(mix_r) if mix_r is not None else None
-        ws = _workspace(workspace, load().wkv4_token_shift_backward_workspace(B, T, C, mix_r is not None),
+        ws = _workspace(workspace, lib.wkv4_token_shift_backward_workspace(B, T, C, mix_r is not None),
                         dev, stream)
-        rc = load().wkv4_token_shift_backward(B, T, C, _ptr(x), _ptr(x_prev), _ptr(mix_k), _ptr(mix_v),
-                                              _ptr(mix_r), _ptr(gxk), _ptr(gxv), _ptr(gxr),
-                                              _ptr(gx_last), _ptr(gx), _ptr(gp), _ptr(gk), _ptr(gv),
-                                              _ptr(gr), _ptr(ws), 0 if ws is None else ws.numel(),
-                                              _stream(stream, dev), dt)
+        rc = lib.wkv4_token_shift_backward(B, T, C, x.data_ptr(), _adr(x_prev), mix_k.data_ptr(),
+                                           mix_v.data_ptr(), _adr(mix_r), gxk.data_ptr(), gxv.data_ptr(),
+                                           _adr(gxr), _adr(gx_last), gx.data_ptr(), _adr(gp),
+                                           gk.data_ptr(), gv.data_ptr(), _adr(gr), _adr(ws),
+                                           0 if ws is None else ws.numel(), _raw_stream(stream, dev), dt)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_token_shift_backward")
     return ShiftGrads(gx, gk, gv, gr, gp)
@@ -602,24 +643,25 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
     if dt is None:
         raise ValueError(f"unsupported dtype {logits.dtype}")
     n = K if n is None else int(n)
-    _check_dev("scores", scores, torch.float32)
-    if finished is not None and finished.dtype not in (torch.bool, torch.uint8):
-        raise ValueError("finished must be bool or uint8")
-    _check_dev("finished", finished)
-    for name, t in (("scores", scores), ("finished", finished)):
-        if t is not None and t.shape != (G, K):
-            raise ValueError(f"{name} must be [G, K]")
+    dev = _cuda("logits", logits)
+    _require(dev, torch.float32, scores=scores)
+    if finished is not None:
+        if finished.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("finished must be bool or uint8")
+        _require(dev, finished.dtype, finished=finished)
+    _shape((G, K), "[G, K]", scores=scores, finished=finished)
     sg, sk, sv = logits.stride()
     ld = sk if K > 1 else sg if G > 1 else V
     if (V > 1 and sv != 1) or ld < V or (G > 1 and K > 1 and sg != K * sk):
         raise ValueError("logits must be rows of unit stride, evenly spaced")
-    dev = _one_device(logits=logits, scores=scores, finished=finished)
-    with torch.cuda.device(dev):
+    lib = load()
+    with _on(dev):
         out = torch.empty((G, max(n, 0)), dtype=torch.float32, device=dev)
-        parents, tokens = (torch.empty((G, max(n, 0)), dtype=torch.int32, device=dev) for _ in range(2))
-        rc = load().wkv4_beam_select(G, K, V, ld, n, _ptr(logits), _ptr(scores), _ptr(finished),
-                                     int(end_id), _ptr(out), _ptr(parents), _ptr(tokens),
-                                     _stream(stream, dev), dt)
+        parents = torch.empty_like(out, dtype=torch.int32)
+        tokens = torch.empty_like(parents)
+        rc = lib.wkv4_beam_select(G, K, V, ld, n, logits.data_ptr(), scores.data_ptr(), _adr(finished),
+                                  int(end_id), out.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
+                                  _raw_stream(stream, dev), dt)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_beam_select")
     return out, parents, tokens
@@ -640,18 +682,18 @@ def state_reorder(pool: torch.Tensor, slot_ids: torch.Tensor, parents: torch.Ten
         raise ValueError(f"unsupported dtype {pool.dtype}")
     if slot_ids.dim() != 2:
         raise ValueError("slot_ids must be [G, K]")
-    _check_dev("pool", pool)
+    dev = _cuda("pool", pool)
     if new_slot_ids is None:
         new_slot_ids = torch.empty_like(slot_ids)
-    for name, t in (("slot_ids", slot_ids), ("parents", parents), ("new_slot_ids", new_slot_ids)):
-        _check_dev(name, t, torch.int32)
-        if t.shape != slot_ids.shape:
-            raise ValueError(f"{name} must be [G, K]")
+    _require(dev, pool.dtype, pool=pool)
+    _require(dev, torch.int32, slot_ids=slot_ids, parents=parents, new_slot_ids=new_slot_ids)
+    _shape(slot_ids.shape, "[G, K]", parents=parents, new_slot_ids=new_slot_ids)
     G, K = slot_ids.shape
-    dev = _one_device(pool=pool, slot_ids=slot_ids, parents=parents, new_slot_ids=new_slot_ids)
-    with torch.cuda.device(dev):
-        rc = load().wkv4_state_reorder(P, S, C, G, K, _ptr(pool), _ptr(slot_ids), _ptr(parents),
-                                       _ptr(new_slot_ids), _stream(stream, dev), dt)
+    lib = load()
+    with _on(dev):
+        rc = lib.wkv4_state_reorder(P, S, C, G, K, pool.data_ptr(), slot_ids.data_ptr(),
+                                    parents.data_ptr(), new_slot_ids.data_ptr(),
+                                    _raw_stream(stream, dev), dt)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_state_reorder")
     return new_slot_ids
