@@ -66,7 +66,7 @@ namespace wkv4 {
 
 constexpr int kBwdC = 64;   // channels a tile
 constexpr int kBwdWarps = 4;    // warps a CTA
-constexpr int kBwdMaxCtas = 8;  // CTAs a cluster
+constexpr int kBwdMaxCtas = 16;  // CTAs a cluster
 constexpr int kBwdPitch = 68;   // sums a row of the chunks' (2 lanes a channel, 2 chunks each, meet no bank twice)
 constexpr int kSumBytes = 12;   // a sum in memory: p, a, b
 
@@ -99,20 +99,29 @@ struct BwdParams {
 };
 
 // Shared memory of the backward kernel: per warp the rows of k, v, gout (and
-// r) as loaded, then the warps' chunk sums [NW], the other CTAs' sums
-// [kBwdMaxCtas] and the sum after a round [2], four barriers and the
-// tensor-memory base.
+// r) as loaded, then the warps' chunk sums [NW], the sum after a round [2],
+// four barriers and the tensor-memory base, and the other CTAs' sums [NC].
 template <typename IO, int L, bool kGate>
 struct BwdLayout {
     static constexpr int kTile = L * kBwdC * (int)sizeof(IO);  // one tensor's rows of a warp
     static constexpr int kWarp = (kGate ? 4 : 3) * kTile;
     static constexpr int kChunks = kBwdWarps * kWarp;
-    static constexpr int kPeers = kChunks + kBwdWarps * kBwdPitch * kSumBytes;
-    static constexpr int kCarry = kPeers + kBwdMaxCtas * kBwdC * kSumBytes;
+    static constexpr int kCarry = kChunks + kBwdWarps * kBwdPitch * kSumBytes;
     static constexpr int kBars = kCarry + 2 * kBwdC * kSumBytes;
-    static constexpr int kBytes = kBars + 5 * 8;
-    // al_t and -al_t y_t of a step's channel pair: 4 columns of tensor memory
+    static constexpr int kPeers = kBars + 6 * 8;
+    // al_t and -al_t y_t of a step's channel pair: 4 columns of tensor memory.
+    // A CTA holds its columns from start to end, and an allocation that cannot
+    // be met waits for another CTA's release.  None has to: a CTA of this
+    // kernel takes at least its columns' share (of 512) of the SM's shared
+    // memory, and of its registers, so whatever set of CTAs an SM takes on --
+    // of this kernel and of the others that hold to either share -- needs no
+    // more columns than there are.
     static constexpr int kColumns = 4 * L;
+    static constexpr int kShare = kColumns * (228 * 1024 / 512) - 1024;  // (1 KB a CTA is the system's)
+    __host__ __device__ static constexpr int bytes(int NC) {
+        return kPeers + NC * kBwdC * kSumBytes > kShare ? kPeers + NC * kBwdC * kSumBytes : kShare;
+    }
+    static_assert(32 * kBwdWarps * 128 >= kColumns * (65536 / 512), "registers below the columns' share");
 };
 
 // Limits of the fixed-reference walk: the spread of a chunk's keys in nats
@@ -436,19 +445,41 @@ __device__ __forceinline__ f2 load_f2(const IO* p) {
 constexpr f2 kSigns = 0x8000000080000000ull;
 
 // A pair's decay and bonus.
+//
+// Step i of a chunk decays by ew[i % 4]: neighbouring floats about e^w whose
+// running product stays within a rounding of e^{(i + 1) w}.  One float for
+// every step would be off by up to 2^-25 a step in one direction, 32 times
+// over along a chunk: the largest error of gw under slow decays.
 struct BwdConsts {
-    f2 ew, eu;
+    f2 ew[4], eu;
     float w[2], u[2];
-    // e^w to half a step of its fp32 value: near 1, where it is applied many
-    // times over, 1 + (e^w - 1) is rounded once
-    __device__ __forceinline__ static float decay(float w) { return fabsf(w) < 0.5f ? 1.f + expm1f(w) : expf(w); }
+    __device__ __forceinline__ static void decays(float w, float (&m)[4]) {
+        // e^w = m0 + l, l the rest that m0 leaves out (known where e^w is near 1;
+        // a fast decay is not applied often enough to need it)
+        float m0 = expf(w), l = 0.f;
+        if (fabsf(w) < 0.5f) {
+            const float x = expm1f(w);
+            m0 = 1.f + x;
+            l = x - (m0 - 1.f);
+        }
+        float c = 0.f;  // what the product so far has left out
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c += l;
+            m[i] = m0 + c;
+            c -= m[i] - m0;
+        }
+    }
     __device__ __forceinline__ BwdConsts(const float* gw, const float* gu, int64_t c, int64_t C) {
+        float m[2][4];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             w[j] = c + j < C ? __ldg(gw + c + j) : 0.f;
             u[j] = c + j < C ? __ldg(gu + c + j) : 0.f;
+            decays(w[j], m[j]);
         }
-        ew = pk(decay(w[0]), decay(w[1]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ew[i] = pk(m[0][i], m[1][i]);
         eu = pk(expf(u[0]), expf(u[1]));
     }
 };
@@ -482,12 +513,20 @@ __device__ __forceinline__ void bwd_summary(const IO* sk, const IO* sv, int col,
     }
     const f2 l2e = pk(kLog2e, kLog2e), nref = pk(-ref.R[0], -ref.R[1]);
     f2 A = 0ull, D = 0ull;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
+    auto step = [&](int i, int s) {
         const f2 e = ex2_2(fma2(load_f2<IO>(sk + i * kBwdC + col), l2e, nref));
-        A = fma2(e, load_f2<IO>(sv + i * kBwdC + col), mul2(cc.ew, A));
-        D = fma2(cc.ew, D, e);
+        A = fma2(cc.ew[s], A, mul2(e, load_f2<IO>(sv + i * kBwdC + col)));
+        D = fma2(cc.ew[s], D, e);
+    };
+    int q = 0;
+#pragma unroll 2
+    for (; q + 4 <= n; q += 4) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) step(q + s, s);
     }
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+        if (q + s < n) step(q + s, s);
     const float Aj[2] = {lo(A), hi(A)}, Dj[2] = {lo(D), hi(D)};
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -588,15 +627,16 @@ __device__ __forceinline__ void bwd_walk_up(const BwdChunk<IO>& ch, const BwdCon
                 st[4 * s + 2] = (uint32_t)nay;
                 st[4 * s + 3] = (uint32_t)(nay >> 32);
                 gu = fma2(mul2(ee, al), add2(v, ny), gu);
-                gw = fma2(al, Ap, fma2(nay, Dp, gw));
+                gw = fma2(al, fma2(ny, Dp, Ap), gw);
                 P = fma2(f, al, P);
                 Q = fma2(f, nay, Q);
-                f = mul2(f, cc.ew);
-                const f2 t1 = mul2(cc.ew, A), t2 = mul2(cc.ew, D);
-                Ap = fma2(cc.ew, Ap, t1);
-                Dp = fma2(cc.ew, Dp, t2);
-                A = fma2(e, v, t1);
-                D = add2(t2, e);
+                f = mul2(f, cc.ew[s]);
+                Ap = mul2(cc.ew[s], add2(Ap, A));
+                Dp = mul2(cc.ew[s], add2(Dp, D));
+                // (one rounding a step: where one key outweighs the rest, A and D
+                // drift apart by it and y D' - A' is what they differ by)
+                A = fma2(cc.ew[s], A, mul2(e, v));
+                D = fma2(cc.ew[s], D, e);
             } else {
                 st[4 * s] = st[4 * s + 1] = st[4 * s + 2] = st[4 * s + 3] = 0;
             }
@@ -636,8 +676,8 @@ __device__ __forceinline__ void bwd_walk_down(const BwdChunk<IO>& ch, const BwdC
                     store_pair(gv + (int64_t)i * C, xv, vec, s0, s1);
                     store_pair(gk + (int64_t)i * C, xk, vec, s0, s1);
                 }
-                P = fma2(cc.ew, P, al);
-                Q = fma2(cc.ew, Q, nay);
+                P = fma2(cc.ew[s & 3], P, al);
+                Q = fma2(cc.ew[s & 3], Q, nay);
             }
         }
     }
@@ -669,7 +709,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
 
     unsigned char* const wbase = smem + warp * Lay::kWarp;
     const Sums chunk(smem + Lay::kChunks, NW * kBwdPitch);
-    const Sums peers(smem + Lay::kPeers, kBwdMaxCtas * kBwdC);  // row q: CTA q's sum (below rank forward, above backward)
+    // CTA q's sums: those of the ranks below this one on the way up, above on the way down
+    auto peer = [&](int q) { return Sums(smem + Lay::kPeers + q * (kBwdC * kSumBytes), kBwdC); };
     const Sums after(smem + Lay::kCarry, 2 * kBwdC);            // (P, Q) after a round, two in turn
     // barriers: the lower ranks' forward sums, the higher ranks' (P, Q), the two rows of `after`
     uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + Lay::kBars);
@@ -799,11 +840,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             const Sum total = lane_sum<P>(y, P - 1);
             Sum ex = lane_sum<P>(y, part - 1);
             if (part == 0) ex = empty_sum();
-            for (int q = rank + 1 + part; q < NC; q += P) push_sum(peers, rank * kBwdC + jc, total, bar, q);
+            for (int q = rank + 1 + part; q < NC; q += P) push_sum(peer(rank), jc, total, bar, q);
             Sum s = carry;  // part 0: the round's start; the others: empty
             if (rank > 0) {
                 wait(0, parity);
-                for (int q = q0; q < min(q1, rank); ++q) s = join(s, peers.get(q * kBwdC + jc), dT);
+                for (int q = q0; q < min(q1, rank); ++q) s = join(s, peer(q).get(jc), dT);
                 s = decayed(s, d_up);
 #pragma unroll
                 for (int h = 1; h < P; h *= 2) s = join(s, lane_sum<P>(s, part ^ h));
@@ -882,7 +923,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             const Sum total = lane_sum<P>(y, 0);
             Sum ex = lane_sum<P>(y, part + 1);
             if (part == P - 1) ex = empty_sum();
-            for (int q = rank - 1 - part; q >= 0; q -= P) push_sum(peers, rank * kBwdC + jc, total, bar + 1, q);
+            for (int q = rank - 1 - part; q >= 0; q -= P) push_sum(peer(rank), jc, total, bar + 1, q);
             // (P, Q) after the round: what rank 0 found last round, or the last
             // state's, carried on to the end of the last round (as if the
             // recurrence ran on there: every chunk is a whole one to the joins)
@@ -900,7 +941,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             }
             if (handed) ++passed;
             if (rank < NC - 1) wait(1, parity);
-            for (int q = q1 - 1; q >= max(q0, rank + 1); --q) s = join(s, peers.get(q * kBwdC + jc), dT);
+            for (int q = q1 - 1; q >= max(q0, rank + 1); --q) s = join(s, peer(q).get(jc), dT);
             s = decayed(s, d_down);
 #pragma unroll
             for (int h = 1; h < P; h *= 2) s = join(s, lane_sum<P>(s, part ^ h));

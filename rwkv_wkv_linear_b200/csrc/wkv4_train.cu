@@ -26,8 +26,11 @@ static BwdShape bwd_shape(int64_t B, int64_t T, int64_t C, int dtype, bool gated
     auto shape = [&](int L) {
         const int64_t ctas = std::max<int64_t>(1, (T + kBwdWarps * L - 1) / (kBwdWarps * L));
         s.L = L;
+        // 8 CTAs a cluster at most, 16 where the clusters are few: a round is then
+        // a chain of latencies, and there are half as many
+        const int most = tiles * kBwdMaxCtas <= 2 * 148 ? kBwdMaxCtas : 8;
         s.NC = 1;
-        while (s.NC < kBwdMaxCtas && s.NC < ctas) s.NC *= 2;
+        while (s.NC < most && s.NC < ctas) s.NC *= 2;
         s.rounds = (ctas + s.NC - 1) / s.NC;
     };
     // Steps a chunk: 32; in fp32 (twice the shared memory, so fewer CTAs an SM)
@@ -81,8 +84,13 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
     using Lay = BwdLayout<IO, L, kGate>;
     auto kern = wkv4_backward_kernel<IO, L, kGate>;
     static DeviceFlags attr;
-    cudaError_t e = ensure_smem_attr(attr, kern, Lay::kBytes);
+    cudaError_t e = ensure_smem_attr(attr, kern, Lay::bytes(kBwdMaxCtas));
     if (e != cudaSuccess) return e;
+    if (sh.NC > 8) {
+        static DeviceFlags wide;
+        e = ensure_attr(wide, kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     const unsigned tiles = (unsigned)((a.C + kBwdC - 1) / kBwdC), threads = 32 * kBwdWarps;
     if (sh.rounds > 1) {
         auto sum = wkv4_backward_summary_kernel<IO, L>;
@@ -102,7 +110,7 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = launch_grid(dim3(tiles * (unsigned)sh.NC, (unsigned)(sh.rows(a.B) / sh.NC)));
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = Lay::kBytes;
+    cfg.dynamicSmemBytes = Lay::bytes(sh.NC);
     cfg.stream = a.stream;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
