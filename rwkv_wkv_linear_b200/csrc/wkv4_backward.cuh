@@ -93,6 +93,7 @@ struct BwdParams {
     float* ck_a;
     float* ck_b;
     uint32_t wait_rounds;  // limit of each bounded wait
+    int no_push;           // checked builds' fault injection: no CTA pushes its sums
     int nb;            // batch rows a cluster walks, one after another
     bool vec_load;     // every row of k, v, gout, r starts on 16 bytes
     bool vec_store;    // channel pairs of gk, gv, gr may be stored as one access
@@ -840,7 +841,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             const Sum total = lane_sum<P>(y, P - 1);
             Sum ex = lane_sum<P>(y, part - 1);
             if (part == 0) ex = empty_sum();
-            for (int q = rank + 1 + part; q < NC; q += P) push_sum(peer(rank), jc, total, bar, q);
+            for (int q = rank + 1 + part; q < NC && !p.no_push; q += P) push_sum(peer(rank), jc, total, bar, q);
             Sum s = carry;  // part 0: the round's start; the others: empty
             if (rank > 0) {
                 wait(0, parity);
@@ -923,7 +924,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             const Sum total = lane_sum<P>(y, 0);
             Sum ex = lane_sum<P>(y, part + 1);
             if (part == P - 1) ex = empty_sum();
-            for (int q = rank - 1 - part; q >= 0; q -= P) push_sum(peer(rank), jc, total, bar + 1, q);
+            for (int q = rank - 1 - part; q >= 0 && !p.no_push; q -= P) push_sum(peer(rank), jc, total, bar + 1, q);
             // (P, Q) after the round: what rank 0 found last round, or the last
             // state's, carried on to the end of the last round (as if the
             // recurrence ran on there: every chunk is a whole one to the joins)
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
                 const Sum x = join(s, total, dT), y0 = scaled(x.a, x.b, x.p);
                 const int slot = (passed & 1) * kBwdC + jc;
                 if (part == P - 1) after.put(slot, y0);
-                for (int q = 1 + part; q < NC; q += P) push_sum(after, slot, y0, bar + 2 + (passed & 1), q);
+                for (int q = 1 + part; q < NC && !p.no_push; q += P) push_sum(after, slot, y0, bar + 2 + (passed & 1), q);
             }
             const Sum R1 = join(s, ex, d_after);
             chunk.put(i1, R1);

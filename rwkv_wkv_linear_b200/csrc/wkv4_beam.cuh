@@ -571,7 +571,8 @@ struct ReorderParams {
     int32_t* new_ids;        // [G][K]
 };
 
-template <typename E>
+// N: planes a thread copies.
+template <typename E, int N>
 __global__ void __launch_bounds__(256) wkv4_state_reorder_kernel(const ReorderParams p) {
     allow_dependents();
     grid_dependency_wait();
@@ -604,25 +605,30 @@ __global__ void __launch_bounds__(256) wkv4_state_reorder_kernel(const ReorderPa
     }
     if (!whole) return;  // a bad id or parent: the group is left as it is
     const int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int64_t plane = (int64_t)blockIdx.y * blockDim.y + threadIdx.y;
-    const bool in = c < p.row && plane < p.P;
-    E* const base = static_cast<E*>(p.pool) + plane * p.S * p.row + c;
-    // four rows in flight a thread
+    const int64_t plane0 = (int64_t)blockIdx.y * blockDim.y * N + threadIdx.y, step = p.S * p.row;
+    E* const base = static_cast<E*>(p.pool) + plane0 * step + c;
+    // four rows of every plane in flight a thread
     for (unsigned left = moved; left;) {
         int32_t from[4], to[4];
-        E x[4];
+        E x[N][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int who = left ? __ffs(left) - 1 : -1;
             from[i] = __shfl_sync(all, src, who & 31);
             to[i] = __shfl_sync(all, dst, who & 31);
-            if (who < 0) to[i] = -1;
+            if (who < 0 || c >= p.row || !in_range(from[i], p.S) || !in_range(to[i], p.S)) to[i] = -1;
             left &= left - 1;
-            if (in && to[i] >= 0 && in_range(from[i], p.S)) x[i] = base[from[i] * p.row];
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                if (to[i] >= 0 && plane0 + q * blockDim.y < p.P)
+                    x[q][i] = base[q * blockDim.y * step + from[i] * p.row];
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (in && to[i] >= 0 && in_range(to[i], p.S)) base[to[i] * p.row] = x[i];
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                if (to[i] >= 0 && plane0 + q * blockDim.y < p.P)
+                    base[q * blockDim.y * step + to[i] * p.row] = x[q][i];
     }
 }
 

@@ -179,6 +179,7 @@ cudaError_t launch_backward(const BwdArgs& a) {
                  aligned(a.r, 16);
     p.vec_store = a.C % 2 == 0 && aligned(a.gk, 2 * es) && aligned(a.gv, 2 * es) && aligned(a.gr, 2 * es);
     p.wait_rounds = wait_rounds();
+    p.no_push = fault_plan().exchange ? 1 : 0;
     if (a.T == 0) {
         const int64_t n = a.B * a.C;
         return launch_pdl(wkv4_backward_no_steps_kernel, launch_grid(dim3((unsigned)((n + 127) / 128))),
