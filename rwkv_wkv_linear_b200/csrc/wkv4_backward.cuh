@@ -418,6 +418,13 @@ __device__ __noinline__ ExactGrads exact_backward_down(const ExactChunk<IO> c, S
     return {R, gw, gu};
 }
 
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_acquire() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Steps of a chunk starting at t.
 __device__ __forceinline__ int chunk_steps(int T, int t, int most) { return max(0, min(most, T - t)); }
 
@@ -471,14 +478,17 @@ struct BwdConsts {
             c -= m[i] - m0;
         }
     }
-    __device__ __forceinline__ BwdConsts(const float* gw, const float* gu, int64_t c, int64_t C) {
-        float m[2][4];
+    __device__ __forceinline__ void load(const float* gw, const float* gu, int64_t c, int64_t C) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             w[j] = c + j < C ? __ldg(gw + c + j) : 0.f;
             u[j] = c + j < C ? __ldg(gu + c + j) : 0.f;
-            decays(w[j], m[j]);
         }
+    }
+    __device__ __forceinline__ void derive() {
+        float m[2][4];
+        decays(w[0], m[0]);
+        decays(w[1], m[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) ew[i] = pk(m[0][i], m[1][i]);
         eu = pk(expf(u[0]), expf(u[1]));
@@ -753,26 +763,32 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             if constexpr (kGate) prefetch_l2(static_cast<const IO*>(p.r) + o);
         }
     };
-    load_item(b0, last);
+    // w and u first: behind the rows' copies they would wait for them
+    const int jc = threadIdx.x / P, part = threadIdx.x % P;
+    const bool jok = c0 + jc < C;
+    const float jw = jok ? __ldg(p.w + c0 + jc) : 0.f;
+    BwdConsts cc;
+    cc.load(p.w, p.u, c, C);
     if (threadIdx.x < 4) mbar_init(bar + threadIdx.x, 1);
     if (threadIdx.x == 0) fence_mbar_init();
     if (warp == 0) tmem_alloc(tslot, Lay::kColumns);
     tmem_fence_before_sync();
-    cluster.sync();  // every CTA's barriers are set up before a peer's sum may arrive
+    __syncthreads();
     tmem_fence_after_sync();
+    // Every CTA's barriers are set up before a peer's sum may arrive.  (Relaxed:
+    // the barriers' own fence is enough, and a release would wait for the rows.)
+    cluster_arrive_relaxed();
+    load_item(b0, last);
     // the lane quarter of tensor memory that this warp reaches
     const uint32_t taddr = *tslot + ((uint32_t)warp << 21);
     BwdChunk<IO> ch{reinterpret_cast<const IO*>(wbase), reinterpret_cast<const IO*>(wbase + Lay::kTile),
                     reinterpret_cast<const IO*>(wbase + 2 * Lay::kTile),
                     reinterpret_cast<const IO*>(wbase + (kGate ? 3 : 2) * Lay::kTile), taddr, col, 0};
 
-    const BwdConsts cc(p.w, p.u, c, C);
+    cc.derive();
     // this thread's part in the joins: chunks 2 part, 2 part + 1 of channel jc,
     // and CTAs q0 .. q0 + qn - 1 of the cluster
-    const int jc = threadIdx.x / P, part = threadIdx.x % P;
-    const bool jok = c0 + jc < C;
-    
-    const Rate rate = rate_of(jok ? p.w[c0 + jc] : 0.f);
+    const Rate rate = rate_of(jw);
     const Decay dL = decay_of(rate, L), d2 = decay_of(rate, 2 * L), d4 = decay_of(rate, 4 * L),
                 dT = decay_of(rate, Ts);
     const Decay d_before = decay_of(rate, 2 * part * L), d_after = decay_of(rate, (NW - 2 - 2 * part) * L);
@@ -781,6 +797,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     // of CTA max(q0, rank + 1) to this CTA's end
     const Decay d_up = decay_of(rate, (rank - min(q1, rank)) * Ts);
     const Decay d_down = decay_of(rate, (max(q0, rank + 1) - (rank + 1)) * Ts);
+    cluster_wait_acquire();
+
     f2 gw_sum = 0ull, gu_sum = 0ull;
     int passed = 0;  // rounds handed on so far: `after` and its barriers take turns
 
@@ -1054,7 +1072,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps) wkv4_backward_summary_kernel(c
     const int64_t C = p.C, BC = p.B * C;
     const int t_warp = (round * NW + warp) * NC * L;
     if (!in_range(b, p.B)) return;
-    const BwdConsts cc(p.w, p.u, c0 + col, C);
+    BwdConsts cc;
+    cc.load(p.w, p.u, c0 + col, C);
     unsigned char* const buf = smem + (size_t)warp * 4 * kTile;  // two stages of k, v
     const Sums chunk(smem + (size_t)NW * 4 * kTile, NW * kBwdC);
     auto load = [&](int q) {
@@ -1066,6 +1085,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) wkv4_backward_summary_kernel(c
         load_rows<IO, L>(d, kv, C, c0, n, lane, p.vec_load);
         cp_async_commit();
     };
+    cc.derive();
     const Decay dL[2] = {decay_of(rate_of(cc.w[0]), L), decay_of(rate_of(cc.w[1]), L)};
     Sum acc[2] = {empty_sum(), empty_sum()};
     load(0);
