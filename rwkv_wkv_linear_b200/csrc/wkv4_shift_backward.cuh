@@ -13,9 +13,13 @@
 // of kShiftBwdStages of its own in shared memory, filled by asynchronous
 // copies: a thread waits for nobody, and what is in flight does not cost
 // registers.  The gm_i partial sums of the CTA's runs are joined in shared
-// memory and written one row a CTA; wkv4_column_sum_kernel adds the rows in a
-// fixed order.  All arithmetic in fp32, rounded once at the stores.
+// memory.  Where the CTAs of one channel block are at most 8 they are one
+// cluster and add up their sums through its shared memory; otherwise each
+// writes a row and wkv4_column_sum_kernel adds the rows.  Both in a fixed
+// order.  All arithmetic in fp32, rounded once at the stores.
 #pragma once
+
+#include <cooperative_groups.h>
 
 #include "wkv4_device.cuh"
 #include "wkv4_shift.cuh"  // load_f32
@@ -31,6 +35,7 @@ struct ShiftBwdParams {
     const void* gx_last;  // [B][C] or NULL
     void* gx;
     void* gx_prev;        // [B][C] or NULL
+    float* gmix[3];       // gm_i, written by the clusters themselves (part NULL), or
     float* part;          // [n][rows][C] partial sums of gm, row (b, y block)
     int64_t rows;
     int64_t run;          // steps a thread walks
@@ -162,14 +167,37 @@ __global__ void __launch_bounds__(kShiftBwdX* kShiftBwdY, kShiftBwdCtas)
 #pragma unroll
         for (int j = 0; j < V; ++j) red[i][threadIdx.y][j * kShiftBwdX + threadIdx.x] = acc[i][j];
     __syncthreads();
-    const int64_t prow = b * gridDim.y + blockIdx.y;
-    for (int q = threadIdx.y; q < N * V; q += kShiftBwdY) {
-        const int i = q / V, j = q % V;
-        float s = 0.f;
+    const int64_t cb = (int64_t)blockIdx.x * kShiftBwdX * V;  // the CTA's first channel
+    if (p.part) {
+        const int64_t prow = b * gridDim.y + blockIdx.y;
+        for (int q = tid; q < N * V * kShiftBwdX; q += kThreads) {
+            const int i = q / (V * kShiftBwdX), x = q % (V * kShiftBwdX);
+            const int64_t ch = cb + (int64_t)(x % kShiftBwdX) * V + x / kShiftBwdX;
+            float s = 0.f;
 #pragma unroll
-        for (int y = 0; y < kShiftBwdY; ++y) s += red[i][y][j * kShiftBwdX + threadIdx.x];
-        if (c + j < p.C) p.part[(i * p.rows + prow) * p.C + c + j] = s;
+            for (int y = 0; y < kShiftBwdY; ++y) s += red[i][y][x];
+            if (ch < p.C) p.part[(i * p.rows + prow) * p.C + ch] = s;
+        }
+        return;
     }
+    // the cluster: all (y, b) of this channel block; CTA r adds every CTA's runs
+    // of its share of the columns
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int n = (int)cluster.num_blocks();
+    cluster.sync();
+    for (int q = tid + kThreads * (int)cluster.block_rank(); q < N * V * kShiftBwdX; q += kThreads * n) {
+        const int i = q / (V * kShiftBwdX), x = q % (V * kShiftBwdX);
+        const int64_t ch = cb + (int64_t)(x % kShiftBwdX) * V + x / kShiftBwdX;
+        float s = 0.f;
+        for (int r = 0; r < n; ++r) {
+            const float* const at = cluster.map_shared_rank(&red[i][0][x], r);
+#pragma unroll
+            for (int y = 0; y < kShiftBwdY; ++y) s += at[y * kShiftBwdX * V];
+        }
+        if (ch < p.C) p.gmix[i][ch] = s;
+    }
+    cluster.sync();  // no CTA leaves while a peer may still read its sums
 }
 
 }  // namespace wkv4

@@ -199,6 +199,10 @@ cudaError_t launch_backward(const BwdArgs& a) {
 struct ShiftBwdShape {
     int V;
     int64_t run, yblocks;
+    // A channel block's CTAs as one cluster: no second kernel (a short call is all
+    // launches: B=2, T=65, C=768 29.8 -> 24.6 us of host time).  Clusters of 16
+    // would leave SMs idle (B=4, T=1024, C=5120: 51.9 us against 46.4).
+    bool one_cluster(int64_t B) const { return yblocks * B <= 8; }
 };
 
 static ShiftBwdShape shift_bwd_shape(int64_t B, int64_t T, int64_t C, bool vec) {
@@ -214,16 +218,34 @@ static ShiftBwdShape shift_bwd_shape(int64_t B, int64_t T, int64_t C, bool vec) 
 }
 
 size_t shift_backward_workspace(int64_t B, int64_t T, int64_t C, int n) {
-    // either channel width may be taken (it depends on the pointers' alignment)
-    const int64_t rows = std::max(shift_bwd_shape(B, T, C, true).yblocks, shift_bwd_shape(B, T, C, false).yblocks);
+    int64_t rows = 0;  // either channel width may be taken (it depends on the pointers' alignment)
+    for (bool vec : {false, true}) {
+        const ShiftBwdShape s = shift_bwd_shape(B, T, C, vec);
+        if (!s.one_cluster(B)) rows = std::max(rows, s.yblocks);
+    }
     return (size_t)n * B * rows * C * 4;
 }
 
 template <typename IO, int V, int N>
 static cudaError_t launch_shift_bwd_t(const ShiftBwdParams& p, const ShiftBwdShape& s, cudaStream_t stream) {
+    auto kern = wkv4_token_shift_backward_kernel<IO, V, N>;
     const dim3 grid((unsigned)((p.C + kShiftBwdX * V - 1) / (kShiftBwdX * V)), (unsigned)s.yblocks, (unsigned)p.B);
-    return launch_pdl(wkv4_token_shift_backward_kernel<IO, V, N>, launch_grid(grid),
-                      dim3(kShiftBwdX, kShiftBwdY), 0, stream, p);
+    const bool one = s.one_cluster(p.B);
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = launch_grid(grid);
+    cfg.blockDim = dim3(kShiftBwdX, kShiftBwdY);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = (unsigned)s.yblocks;
+    at[1].val.clusterDim.z = (unsigned)p.B;
+    cfg.attrs = at;
+    cfg.numAttrs = one ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <typename IO>
@@ -254,7 +276,8 @@ cudaError_t launch_shift_backward(const ShiftBwdArgs& a) {
         p.mix[i] = a.mix[i];
         p.g[i] = a.g[i];
     }
-    p.part = static_cast<float*>(a.workspace);
+    for (int i = 0; i < n; ++i) p.gmix[i] = a.gmix[i];
+    p.part = s.one_cluster(a.B) ? nullptr : static_cast<float*>(a.workspace);
     p.rows = a.B * s.yblocks;
     p.run = s.run;
     cudaError_t e;
@@ -263,7 +286,7 @@ cudaError_t launch_shift_backward(const ShiftBwdArgs& a) {
         case WKV4_F16: e = launch_shift_bwd_io<__half>(p, s, n, a.stream); break;
         default: e = launch_shift_bwd_io<__nv_bfloat16>(p, s, n, a.stream); break;
     }
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || !p.part) return e;
     return launch_column_sum(p.part, a.gmix[0], a.gmix[1], a.gmix[2], n, p.rows, a.C, a.stream);
 }
 

@@ -138,14 +138,20 @@ def _sb(B=2, T=8, C=16, x=P + 0x10000, xp=None, mk=P, mv=P + 0x1000, mr=None, gx
 def test_token_shift_backward_argument_checks():
     assert _sb(B=-1) == -1 and _sb(T=-1) == -1 and _sb(C=-1) == -1 and _sb(dtype=3) == -2
     assert _sb(C=0) == 0
-    for name in ("x", "mk", "mv", "gxk", "gxv", "gx", "gmk", "gmv", "ws"):
+    for name in ("x", "mk", "mv", "gxk", "gxv", "gx", "gmk", "gmv"):
         assert _sb(**{name: None}) == -1, name
     assert _sb(mr=P + 0x4000) == -1 and _sb(mr=P + 0x4000, gmr=P + 0x5000) == -1   # no gxr
     assert _sb(B=70000) == -1
-    need = wkv4.load().wkv4_token_shift_backward_workspace(2, 8, 16, 0)
-    assert _sb(nbytes=need - 1) == -1 and _sb(ws=P + 0x100008) == -1
+    sizes = wkv4.load().wkv4_token_shift_backward_workspace
+    assert sizes(2, 8, 16, 0) == 0             # few enough rows to be summed by one cluster
+    need = sizes(20, 8, 16, 0)
+    far = dict(B=20, x=P + 0x1000000, gxk=P + 0x2000000, gxv=P + 0x3000000, gx=P + 0x4000000, ws=P + 0x5000000)
+    assert need > 0 and _sb(**far, nbytes=need - 1) == -1
+    far["ws"] += 8
+    assert _sb(**far) == -1
     assert _sb(gx=P + 0x20000) == -3 and _sb(gmv=P + 0x2000) == -3 and _sb(gmk=P + 16) == -3
-    assert _sb(ws=P + 0x40000 + 64) == -3
+    far["ws"] = P + 0x4000000 + 64             # the workspace over gx
+    assert _sb(**far) == -3
 
 
 def test_binding_refuses_host_and_mismatched_tensors():
