@@ -224,9 +224,11 @@ def _code_only(text: str) -> str:
     return "\n".join(line.rstrip() for line in out.splitlines() if line.strip())
 
 
-# host code that launches nothing of its own: the host-buffer pipeline only
-# chains the forward's calls, so it does not change a kernel's traffic
-_NOT_KERNEL_SOURCES = {"wkv4_host.cpp"}
+# sources without a kernel of the bench's workloads: the host-buffer pipeline
+# only chains the forward's calls, and the backward and beam search kernels are
+# translation units of their own
+_NOT_KERNEL_SOURCES = {"wkv4_host.cpp", "wkv4_train.cu", "wkv4_backward.cuh", "wkv4_shift_backward.cuh",
+                       "wkv4_beam.cu", "wkv4_beam.cuh"}
 
 
 def kernel_source_hash(csrc=None):

@@ -162,3 +162,25 @@ def test_binding_refuses_host_and_mismatched_tensors():
         wkv4.backward(k, k, torch.zeros(8), torch.zeros(8), torch.zeros(1, 3, 8))
     with pytest.raises(ValueError):
         wkv4.token_shift_backward(k, torch.zeros(8), torch.zeros(8), k, k, mix_r=torch.zeros(8))
+
+
+def test_kernel_hash_leaves_out_the_units_the_bench_does_not_launch(tmp_path):
+    """The recorded traffic of the bench's workloads is keyed by the sources of
+    their kernels: the backward and beam search units are not among them, and
+    the forward's kernels include none of their files."""
+    import os
+    import shutil
+
+    import bench
+    csrc = os.path.join(bench.ROOT, "rwkv_wkv_linear_b200", "csrc")
+    copy = tmp_path / "csrc"
+    shutil.copytree(csrc, copy)
+    base = bench.kernel_source_hash(str(copy))
+    for name in bench._NOT_KERNEL_SOURCES:
+        f = copy / name
+        f.write_text(f.read_text() + "\nstatic const int one_more_constant = 3;\n")
+    assert bench.kernel_source_hash(str(copy)) == base
+    for name in os.listdir(csrc):
+        if name not in bench._NOT_KERNEL_SOURCES:
+            text = (copy / name).read_text()
+            assert not any(f'#include "{other}"' in text for other in bench._NOT_KERNEL_SOURCES), name
