@@ -326,8 +326,8 @@ WKV4_API size_t wkv4_forward_host_workspace(int64_t B, int64_t T, int64_t C, int
  * WKV4_ERR_ALIAS.  T == 0: gstate_in <- gstate_out's share (the state passes
  * through), gw = gu = 0.  B == 0 or C == 0: nothing is written but gw and gu
  * (zero).  A NULL required pointer, a workspace that is too small or
- * misaligned, or T above 2^24 steps: WKV4_ERR_ARG.  Asynchronous on `stream`;
- * no allocation.
+ * misaligned, T above 2^24, B above 65535 or C above 4194240: WKV4_ERR_ARG.
+ * Asynchronous on `stream`; no allocation.
  */
 WKV4_API int wkv4_backward(int64_t B, int64_t T, int64_t C, const float* w, const float* u,
                            const void* k, const void* v, const void* r, const float* state_in,
@@ -356,7 +356,8 @@ WKV4_API size_t wkv4_backward_workspace(int64_t B, int64_t T, int64_t C, int dty
  *                  (the gradient by a previous token that was zero).
  *   gmix_k, gmix_v, gmix_r  [C] fp32, summed in fp32 in a fixed order.
  *   workspace      device memory of at least wkv4_token_shift_backward_workspace
- *                  (B, T, C, mix_r != NULL) bytes, 16-byte aligned.
+ *                  (B, T, C, mix_r != NULL) bytes, 16-byte aligned
+ *                  (may be NULL where that is 0).
  * T == 0: gx_prev <- gx_last (or zero), the gmix zero.  Limits on B and T,
  * overlaps and errors as wkv4_token_shift and wkv4_backward.
  */

@@ -360,7 +360,7 @@ int wkv4_backward(int64_t B, int64_t T, int64_t C, const float* w, const float* 
     if (!gw || !gu) return WKV4_ERR_ARG;
     if (B > 0 && (!w || (gstate_out && !state_out) || (gstate_in && !state_in))) return WKV4_ERR_ARG;
     if (B > 0 && T > 0 && (!u || !k || !v || !gy || !gk || !gv || (r && !gr))) return WKV4_ERR_ARG;
-    if (T > kMaxBackwardSteps || B > 65535 || !fits_grid(16, (C + 63) / 64)) return WKV4_ERR_ARG;
+    if (T > kMaxBackwardSteps || B > 65535 || C > 65535ll * 64) return WKV4_ERR_ARG;
     const size_t need = wkv4_backward_workspace(B, T, C, dtype);
     if (need > 0 && (!workspace || workspace_bytes < need || !is_aligned(workspace, 16)))
         return WKV4_ERR_ARG;

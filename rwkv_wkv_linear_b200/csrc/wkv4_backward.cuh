@@ -94,6 +94,7 @@ struct BwdParams {
     float* ck_b;
     uint32_t wait_rounds;  // limit of each bounded wait
     int no_push;           // checked builds' fault injection: no CTA pushes its sums
+    int NC;            // CTAs a cluster
     int nb;            // batch rows a cluster walks, one after another
     bool vec_load;     // every row of k, v, gout, r starts on 16 bytes
     bool vec_store;    // channel pairs of gk, gv, gr may be stored as one access
@@ -705,16 +706,16 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     constexpr unsigned kAll = 0xffffffffu;
     extern __shared__ __align__(16) unsigned char smem[];
     cg::cluster_group cluster = cg::this_cluster();
-    const int NC = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int NC = p.NC, rank = (int)cluster.block_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 2 * lane;
-    const int c0 = (int)(blockIdx.x >> (__ffs(NC) - 1)) * kBwdC;
+    const int c0 = (int)blockIdx.y * kBwdC;  // grid: the cluster's CTAs, channel tiles, batch rows
     const int T = (int)p.T, rounds = p.rounds, last = rounds - 1;
     const int64_t C = p.C, BC = p.B * C;
     const int round_steps = NC * Ts;
     const int64_t c = c0 + col;
     const bool ok0 = c < C, ok1 = c + 1 < C;
     // the batch rows of this cluster, each walked from its last round to its first
-    const int b0 = blockIdx.y * p.nb, items = min(p.nb, (int)p.B - b0) * rounds;
+    const int b0 = blockIdx.z * p.nb, items = min(p.nb, (int)p.B - b0) * rounds;
     // every global access below is (b T + t) C + c for b < B, t < T, c < C, or b C + c
     if (!in_range(b0, p.B)) return;
 
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     const Decay dL = decay_of(rate, L), d2 = decay_of(rate, 2 * L), d4 = decay_of(rate, 4 * L),
                 dT = decay_of(rate, Ts);
     const Decay d_before = decay_of(rate, 2 * part * L), d_after = decay_of(rate, (NW - 2 - 2 * part) * L);
-    const int qn = max(1, NC / P), q0 = min(part * qn, NC), q1 = min(q0 + qn, NC);
+    const int qn = (NC + P - 1) / P, q0 = min(part * qn, NC), q1 = min(q0 + qn, NC);
     // from the end of CTA min(q1, rank) - 1 to this CTA's start; from the start
     // of CTA max(q0, rank + 1) to this CTA's end
     const Decay d_up = decay_of(rate, (rank - min(q1, rank)) * Ts);
@@ -1051,7 +1052,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             float s = 0.f;
 #pragma unroll
             for (int q = 0; q < NW; ++q) s += red[(which * NW + q) * kBwdC + ci];
-            (which ? p.part_u : p.part_w)[((int64_t)blockIdx.y * NC + rank) * C + c0 + ci] = s;
+            (which ? p.part_u : p.part_w)[((int64_t)blockIdx.z * NC + rank) * C + c0 + ci] = s;
         }
     }
     // (the barriers above are behind every warp's last access to tensor memory)

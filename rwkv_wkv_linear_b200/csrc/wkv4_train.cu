@@ -27,11 +27,11 @@ static BwdShape bwd_shape(int64_t B, int64_t T, int64_t C, int dtype, bool gated
         const int64_t ctas = std::max<int64_t>(1, (T + kBwdWarps * L - 1) / (kBwdWarps * L));
         s.L = L;
         // 8 CTAs a cluster at most, 16 where the clusters are few: a round is then
-        // a chain of latencies, and there are half as many
+        // a chain of latencies, and there are half as many.  No more of them
+        // than the rounds need: a CTA without steps keeps its place all the same.
         const int most = tiles * kBwdMaxCtas <= 2 * 148 ? kBwdMaxCtas : 8;
-        s.NC = 1;
-        while (s.NC < most && s.NC < ctas) s.NC *= 2;
-        s.rounds = (ctas + s.NC - 1) / s.NC;
+        s.rounds = (ctas + most - 1) / most;
+        s.NC = (int)((ctas + s.rounds - 1) / s.rounds);
     };
     // Steps a chunk: 32; in fp32 (twice the shared memory, so fewer CTAs an SM)
     // 16 unless the CTAs are few and walk several rounds, whose joins are then
@@ -108,7 +108,7 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
     }
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = launch_grid(dim3(tiles * (unsigned)sh.NC, (unsigned)(sh.rows(a.B) / sh.NC)));
+    cfg.gridDim = launch_grid(dim3((unsigned)sh.NC, tiles, (unsigned)(sh.rows(a.B) / sh.NC)));
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = Lay::bytes(sh.NC);
     cfg.stream = a.stream;
@@ -174,6 +174,7 @@ cudaError_t launch_backward(const BwdArgs& a) {
         p.ck_b = p.ck_a + n;
     }
     const size_t es = dtype_size(a.dtype);
+    p.NC = sh.NC;
     p.nb = sh.nb;
     p.vec_load = (a.C * es) % 16 == 0 && aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.gy, 16) &&
                  aligned(a.r, 16);

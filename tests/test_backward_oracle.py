@@ -102,6 +102,8 @@ def test_backward_argument_checks():
     assert _bwd(dtype=4) == -2
     assert _bwd(C=0) == 0
     assert _bwd(T=(1 << 24) + 1) == -1
+    assert _bwd(B=65536, T=1, nbytes=1 << 45) == -1  # the grid's two short sides: rows and tiles of 64 channels
+    assert _bwd(C=65535 * 64 + 1, T=1, nbytes=1 << 45) == -1
     for name in ("w", "u", "k", "v", "gy", "gk", "gv", "gw", "gu", "ws"):
         assert _bwd(**{name: None}) == -1, name
     assert _bwd(r=P + 0x60000) == -1                                  # r without gr

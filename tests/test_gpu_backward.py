@@ -70,7 +70,8 @@ def _check(x, g, s_out, dt, what):
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
 @pytest.mark.parametrize("shape", [(1, 1, 8), (2, 3, 7), (1, 16, 64), (2, 17, 66), (3, 65, 130), (1, 130, 72),
-                                   (2, 500, 33), (1, 1024, 64), (2, 1025, 40), (1, 2500, 24)],
+                                   (2, 300, 72), (2, 500, 33), (1, 700, 130), (1, 1024, 64), (2, 1025, 40), (1, 2500, 24),
+                                   (1, 5200, 9)],
                          ids=lambda s: "B%dT%dC%d" % s)
 def test_gradients_match_oracle(cuda_device, shape, gated, dt):
     B, T, C = shape

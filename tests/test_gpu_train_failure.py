@@ -35,7 +35,7 @@ def test_checked_build_records_nothing_on_valid_shapes(cuda_device):
     _child("clean")
 
 
-@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 6, 7, 8])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 6, 7, 8, 9])
 def test_injected_launch_failure(cuda_device, n):
     _child("launch", str(n), WKV4_FAULT=f"launch:{n}")
 

@@ -87,7 +87,7 @@ def clean():
     for dt in ("f32", "f16", "bf16"):
         for shape in ((1, 1, 8), (2, 77, 66), (3, 300, 27), (1, 2100, 72)):
             backward(*shape, dt, gated=shape[1] % 2 == 1)
-        for shape in ((1, 1, 8), (2, 77, 66), (3, 301, 64)):
+        for shape in ((1, 1, 8), (2, 77, 66), (3, 301, 64), (9, 33, 24)):
             shift(*shape, dt)
         for shape in ((1, 1, 5, 3), (2, 3, 5003, 9), (1, 4, 50277, 8)):
             select(*shape, dt)
@@ -96,9 +96,11 @@ def clean():
     assert wkv4.device_error(reset=True) == 0
 
 
-# launches a call makes: several rounds (summary, prefix, main, sums), the shift's two, one each
-CALLS = [(4, lambda: backward(1, 2100, 72, "bf16")), (2, lambda: shift(2, 77, 66, "f16")),
-         (1, lambda: select(2, 3, 1000, 5, "f32")), (1, lambda: reorder(3, 9, 64, 1, 4, "f32"))]
+# launches a call makes: several rounds (summary, prefix, main, sums), the shift's two
+# (CTAs of more rows than a cluster takes) or one, one each
+CALLS = [(4, lambda: backward(1, 2100, 72, "bf16")), (2, lambda: shift(9, 77, 66, "f16")),
+         (1, lambda: select(2, 3, 1000, 5, "f32")), (1, lambda: reorder(3, 9, 64, 1, 4, "f32")),
+         (1, lambda: shift(2, 77, 66, "f16"))]
 
 
 def launch(nth):
