@@ -12,9 +12,9 @@ namespace wkv4 {
 template <typename IO>
 static cudaError_t launch_beam_select_t(const BeamParams& p, int64_t G, int R, cudaStream_t stream) {
     auto kern = wkv4_beam_select_kernel<IO>;
-    // the merge holds every unit's candidates twice
-    const size_t cands = 2 * (size_t)p.K * p.S * p.n * sizeof(BeamCand);
-    const size_t most = sizeof(BeamShared) + 2 * (size_t)kBeamMaxK * kBeamMaxN * sizeof(BeamCand);
+    // the merge holds every unit's candidates
+    const size_t cands = (size_t)p.K * p.S * p.n * sizeof(BeamCand);
+    const size_t most = sizeof(BeamShared) + (size_t)kBeamMaxK * kBeamMaxN * sizeof(BeamCand);
     static DeviceFlags attr, wide;
     cudaError_t e = ensure_smem_attr(attr, kern, most);
     if (e != cudaSuccess) return e;

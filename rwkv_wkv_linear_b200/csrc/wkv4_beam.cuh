@@ -87,7 +87,9 @@ struct alignas(16) BeamShared {
     alignas(16) uint64_t list[kBeamList + 2];
     int32_t piece_at[kBeamPieces];
     uint64_t best[kBeamMaxN];
-    double lse[kBeamMaxK];
+    double lse[kBeamMaxK];   // log-sum of a live beam's row, NaN: no candidates
+    float score[kBeamMaxK];
+    bool ended[kBeamMaxK];   // finished beams
     alignas(16) uint32_t top[kBeamThreads];  // the threads' first maxima at or above the loose bound
     uint32_t wbound[kBeamWarps];
     float wref[kBeamWarps];
@@ -234,16 +236,28 @@ __device__ __forceinline__ void beam_load(const BeamRow<IO>& r, int batch, int t
     }
 }
 
+// The q-th largest of a warp's keys.
+__device__ __forceinline__ uint32_t beam_warp_top(uint32_t key, int q) {
+    uint32_t top = 0;
+    for (; q > 0; --q) {
+        top = __reduce_max_sync(0xffffffffu, key);
+        const unsigned who = __ballot_sync(0xffffffffu, key == top);
+        if ((int)(threadIdx.x & 31) == __ffs(who) - 1) key = 0;
+    }
+    return top;
+}
+// The least of the warps' bounds.
+__device__ __forceinline__ uint32_t beam_least(const BeamShared& s) {
+    uint32_t least = s.wbound[0];
+#pragma unroll
+    for (int q = 1; q < kBeamWarps; ++q) least = min(least, s.wbound[q]);
+    return least;
+}
+
 // The n-th largest of the threads' keys (n <= 256).
 __device__ __forceinline__ uint32_t beam_bound(BeamShared& s, uint32_t key, int n) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per_warp = (n + kBeamWarps - 1) / kBeamWarps;
-    uint32_t mine = key, top = 0;
-    for (int q = 0; q < per_warp; ++q) {
-        top = __reduce_max_sync(0xffffffffu, mine);
-        const unsigned who = __ballot_sync(0xffffffffu, mine == top);
-        if (lane == __ffs(who) - 1) mine = 0;
-    }
+    const uint32_t top = beam_warp_top(key, (n + kBeamWarps - 1) / kBeamWarps);
     if (lane == 0) s.wbound[warp] = top;
     if (tid == 0) {
         s.tops = 0;
@@ -251,9 +265,7 @@ __device__ __forceinline__ uint32_t beam_bound(BeamShared& s, uint32_t key, int 
         s.npieces = 0;
     }
     __syncthreads();
-    uint32_t loose = s.wbound[0];
-#pragma unroll
-    for (int q = 1; q < kBeamWarps; ++q) loose = min(loose, s.wbound[q]);
+    const uint32_t loose = beam_least(s);
     // (equal keys need no order: the n-th largest value lies where those above
     // it are fewer than n and those at or above it n or more)
     s.top[tid] = 0;
@@ -302,7 +314,7 @@ __device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int 
 #pragma unroll
     for (int i = 0; i < kBeamBatch; ++i) m = fmaxf(m, V::max(x0[i]));
     const float bound = key_value((uint64_t)beam_bound(s, ordered(m), n) << 32);
-    const float most = fmaxf(bound, -3.402823466e38f);  // (-inf is no candidate)
+    float most = fmaxf(bound, -3.402823466e38f);  // (-inf is no candidate)
 
     auto take = [&](float x, int at) {
         if (x >= most) {
@@ -362,7 +374,13 @@ __device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int 
         s.wref[warp] = ref;
         s.wsum[warp] = d;
     }
+    {
+        const uint32_t top = beam_warp_top(ordered(sum.max), (n + kBeamWarps - 1) / kBeamWarps);
+        if (lane == 0) s.wbound[warp] = top;
+    }
     __syncthreads();
+    // by now the threads' largest logits are those of the whole unit
+    most = fmaxf(most, key_value((uint64_t)beam_least(s) << 32));
     const int pieces = s.npieces;
     for (int i = tid; i < min(pieces, kBeamPieces) * V::E; i += kBeamThreads)
         take(Io<IO>::to_f(reinterpret_cast<const IO*>(s.pieces())[i]), row.at(s.piece_at[i / V::E], i % V::E));
@@ -435,9 +453,6 @@ struct alignas(16) BeamCand {
     uint64_t key;
     uint32_t flat;
     float score;
-    __device__ __forceinline__ bool before(const BeamCand& o) const {
-        return (key > o.key) | ((key == o.key) & (flat < o.flat));
-    }
 };
 
 template <typename IO>
@@ -468,14 +483,19 @@ __global__ void __launch_bounds__(kBeamThreads, 3) wkv4_beam_select_kernel(const
                       p.n, p.scores + row, p.finished ? p.finished + row : nullptr, &first->units[q], ready);
     }
     ready();
+    if (rank == 0 && tid < p.K) {
+        const float score = p.scores[g * p.K + tid];
+        const bool ended = p.finished && p.finished[g * p.K + tid];
+        s.score[tid] = score;
+        s.ended[tid] = ended;
+    }
     cluster.sync();
     if (rank != 0) return;
 
-    // the rows' log-sums (NaN: no candidates)
+    // the rows' log-sums
     if (tid < p.K) {
-        const float score = p.scores[g * p.K + tid];
         double lse = (double)NAN;
-        if (beam_alive(score) && !(p.finished && p.finished[g * p.K + tid])) {
+        if (beam_alive(s.score[tid]) && !s.ended[tid]) {
             const BeamUnit* u = s.units + tid * p.S;
             float ref = -INFINITY;
             for (int q = 0; q < p.S; ++q) ref = fmaxf(ref, u[q].ref);
@@ -486,15 +506,16 @@ __global__ void __launch_bounds__(kBeamThreads, 3) wkv4_beam_select_kernel(const
         }
         s.lse[tid] = lse;
     }
-    if (tid == 0) s.count = 0;
     __syncthreads();
-    // candidates: every unit's list, or a finished beam's one
-    BeamCand* const all = reinterpret_cast<BeamCand*>(s.pieces());  // [units n], free now
-    for (int e = tid; e < units * p.n; e += kBeamThreads) {
+    // candidates: every unit's list, or a finished beam's one; best first, the rest 0
+    BeamCand* const all = reinterpret_cast<BeamCand*>(s.pieces());  // [units][n], free now
+    const int total = units * p.n;
+    int found = 0;
+    for (int e = tid; e < total; e += kBeamThreads) {
         const int q = e / p.n, j = e - q * p.n, k = q / p.S;
-        const float score = p.scores[g * p.K + k];
+        const float score = s.score[k];
         BeamCand c{0, 0xffffffffu, -INFINITY};
-        if (p.finished && p.finished[g * p.K + k]) {
+        if (s.ended[k]) {
             if (j == 0 && q == k * p.S && beam_alive(score))
                 c = {ordered64((double)score), (uint32_t)(k * p.V) + (uint32_t)p.end_id, score};
         } else if (s.lse[k] == s.lse[k] && j < s.units[q].count) {
@@ -503,31 +524,44 @@ __global__ void __launch_bounds__(kBeamThreads, 3) wkv4_beam_select_kernel(const
             c = {ordered64(x), (uint32_t)(k * p.V) + ~(uint32_t)key, (float)x};
         }
         all[e] = c;
+        found += c.key != 0;
     }
+    found = __reduce_add_sync(0xffffffffu, found);
+    if (lane == 0) s.wkey[tid >> 5] = (uint64_t)found;
     __syncthreads();
-    // at least n candidates lie at or above the least of the units' (n / units)-th best
-    const int per_unit = (p.n + units - 1) / units;
-    uint64_t loose = ~0ull;
-    for (int q = 0; q < units; ++q) loose = min(loose, all[q * p.n + per_unit - 1].key);
-    BeamCand* const some = all + units * p.n;
-    for (int e = tid; e < units * p.n; e += kBeamThreads) {
-        const BeamCand c = all[e];
-        if (c.key != 0 && c.key >= loose) some[atomicAdd(&s.count, 1)] = c;
-    }
-    __syncthreads();
-    const int count = s.count, have = min(count, p.n);
+    found = 0;
+#pragma unroll
+    for (int q = 0; q < kBeamWarps; ++q) found += (int)s.wkey[q];
+    // a candidate's rank: its place in its own list and, by bisection, the
+    // number before it in each other (equal scores: the lower unit's first).
+    // `share` threads a candidate divide the other lists.
+    int share = 1, span = 1;
+    while (share < 32 && share < units && 2 * share * total <= kBeamThreads) share *= 2;
+    while (2 * span <= p.n) span *= 2;
+    const int have = min(found, p.n);
     const int64_t out = g * p.n;
-    for (int e = tid; e < count; e += kBeamThreads) {
-        const BeamCand c = some[e];
-        int above = 0;
-#pragma unroll 8
-        for (int q = 0; q < count; ++q) above += some[q].before(c);
-        if (above < p.n) {
+    for (int e0 = 0; e0 < total; e0 += kBeamThreads / share) {
+        const int e = e0 + tid / share;
+        const BeamCand c = e < total ? all[e] : BeamCand{0, 0, 0.f};
+        const int q = e / p.n;
+        int before = 0;
+        if (c.key != 0) {
+            for (int o = tid & (share - 1); o < units; o += share) {
+                const BeamCand* const list = all + o * p.n;
+                const uint64_t limit = c.key + (o >= q);  // (keys of numbers are below 2^64 - 1)
+                int at = 0;
+                for (int step = span; step > 0; step >>= 1)
+                    if (at + step <= p.n && list[at + step - 1].key >= limit) at += step;
+                before += o == q ? e - q * p.n : at;
+            }
+        }
+        for (int o = share / 2; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        if (c.key != 0 && before < p.n && (tid & (share - 1)) == 0) {
             const uint32_t k = c.flat / (uint32_t)p.V;
-            p.out_scores[out + above] = c.score;
-            p.out_parents[out + above] = (int32_t)k;
-            p.out_tokens[out + above] = (int32_t)(c.flat - k * (uint32_t)p.V);
-            s.best[above] = c.flat;
+            p.out_scores[out + before] = c.score;
+            p.out_parents[out + before] = (int32_t)k;
+            p.out_tokens[out + before] = (int32_t)(c.flat - k * (uint32_t)p.V);
+            s.best[before] = c.flat;
         }
     }
     if (have == p.n) return;
