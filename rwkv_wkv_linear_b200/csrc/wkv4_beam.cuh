@@ -387,7 +387,7 @@ __device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int 
     ready();
     __syncthreads();
     const int count = pieces <= kBeamPieces ? s.count : kBeamList + 1;
-    if (warp == 0) {
+    if (warp == kBeamWarps - 1) {  // (the first warps rank)
         const float r0 = lane < kBeamWarps ? s.wref[lane] : -INFINITY;
         float r = r0;
 #pragma unroll
@@ -546,13 +546,18 @@ __global__ void __launch_bounds__(kBeamThreads, 3) wkv4_beam_select_kernel(const
         const int q = e / p.n;
         int before = 0;
         if (c.key != 0) {
-            for (int o = tid & (share - 1); o < units; o += share) {
-                const BeamCand* const list = all + o * p.n;
-                const uint64_t limit = c.key + (o >= q);  // (keys of numbers are below 2^64 - 1)
-                int at = 0;
+            for (int o0 = tid & (share - 1); o0 < units; o0 += 4 * share) {
+                int at[4] = {};  // four lists at a time
                 for (int step = span; step > 0; step >>= 1)
-                    if (at + step <= p.n && list[at + step - 1].key >= limit) at += step;
-                before += o == q ? e - q * p.n : at;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int o = o0 + i * share, next = at[i] + step;
+                        // (keys of numbers are below 2^64 - 1)
+                        if (o < units && next <= p.n && all[o * p.n + next - 1].key >= c.key + (o >= q))
+                            at[i] = next;
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) before += o0 + i * share == q ? e - q * p.n : at[i];
             }
         }
         for (int o = share / 2; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
