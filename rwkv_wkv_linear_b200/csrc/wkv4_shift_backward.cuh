@@ -6,13 +6,16 @@
 //   gx_prev[b] = sum_i (1 - m_i) g_i[b,0],
 //   gm_i       = sum_{b,t} g_i[b,t] (x[b,t] - x[b,t-1]).
 //
-// An HBM stream: a thread owns V channels of one batch row and walks a run of
-// steps with the row before in registers (x[t-1], and sum_i m_i g_i[t-1], which
-// waits for the next row's share before it is stored), so every input is read
-// once (plus one row a run) and gx written once.  Its rows come through a ring
-// of kShiftBwdStages of its own in shared memory, filled by asynchronous
-// copies: a thread waits for nobody, and what is in flight does not cost
-// registers.  The gm_i partial sums of the CTA's runs are joined in shared
+// An HBM stream: a thread owns V channels of one batch row (as packed pairs) and
+// walks a run of steps with the row before in registers (x[t-1], and
+// sum_i m_i g_i[t-1], which waits for the next row's share before it is stored),
+// so every input is read once (plus one row a run) and gx written once.  Its
+// rows come through a ring of a few rows of its own in shared memory, filled by
+// asynchronous copies: a thread waits for nobody, and what is in flight does not
+// cost registers.  What counts for HBM is the bytes a warp reads in a row: with
+// 8 channels of 16 bits (512 bytes) B=4, T=1024, C=5120 takes 39.8 us (5.3 TB/s
+// of the 210 MB, the column sums' launch included), with 4 (256 bytes) 47.1,
+// whatever the number of instructions.  The gm_i partial sums of the CTA's runs are joined in shared
 // memory.  Where the CTAs of one channel block are at most 8 they are one
 // cluster and add up their sums through its shared memory; otherwise each
 // writes a row and wkv4_column_sum_kernel adds the rows.  Both in a fixed
@@ -22,6 +25,7 @@
 #include <cooperative_groups.h>
 
 #include "wkv4_device.cuh"
+#include "wkv4_chunk.cuh"  // packed f32x2
 #include "wkv4_shift.cuh"  // load_f32
 
 namespace wkv4 {
@@ -43,23 +47,50 @@ struct ShiftBwdParams {
 
 constexpr int kShiftBwdX = 32;  // channel groups a CTA
 constexpr int kShiftBwdY = 4;   // runs a CTA
-template <typename IO> constexpr int kShiftBwdStages = sizeof(IO) == 2 ? 8 : 4;  // 32 KB of rows a CTA
-constexpr int kShiftBwdCtas = 5;  // CTAs an SM (shared memory, and 96 registers a thread)
+constexpr int kShiftBwdWide = 8;  // channels a thread of the wide form (16-bit types: 16 bytes a row)
+// CTAs an SM, by shared memory and registers
+__host__ __device__ constexpr int shift_bwd_ctas(int V) { return V == kShiftBwdWide ? 3 : 5; }
+// rows of a thread in flight: 32 KB a CTA
+__host__ __device__ constexpr int shift_bwd_stages(int piece) { return piece == 16 ? 4 : 8; }
 
 template <int kBytes>
 __device__ __forceinline__ void shift_copy(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+    if constexpr (kBytes == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+    }
+}
+
+// V channels as packed pairs (V == 1: the upper half zero).
+template <int V>
+__device__ __forceinline__ void to_pairs(const float (&x)[V], f2 (&y)[(V + 1) / 2]) {
+#pragma unroll
+    for (int j = 0; j < (V + 1) / 2; ++j) y[j] = pk(x[2 * j], 2 * j + 1 < V ? x[2 * j + 1 < V ? 2 * j + 1 : 0] : 0.f);
+}
+template <typename IO, int V>
+__device__ __forceinline__ void load_pairs(const IO* p, f2 (&y)[(V + 1) / 2]) {
+    float x[V];
+    load_vec<IO, V>(p, x);
+    to_pairs(x, y);
+}
+template <typename IO, int V>
+__device__ __forceinline__ void store_pairs(IO* p, const f2 (&y)[(V + 1) / 2]) {
+    float x[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = j % 2 ? hi(y[j / 2]) : lo(y[j / 2]);
+    store_vec<IO, V>(p, x);
 }
 
 // V > 1: every row of every tensor starts on V elements.
 template <typename IO, int V, int N>
-__global__ void __launch_bounds__(kShiftBwdX* kShiftBwdY, kShiftBwdCtas)
+__global__ void __launch_bounds__(kShiftBwdX* kShiftBwdY, shift_bwd_ctas(V))
     wkv4_token_shift_backward_kernel(const ShiftBwdParams p) {
     allow_dependents();
     grid_dependency_wait();
     constexpr bool kRing = V > 1;
     constexpr int kThreads = kShiftBwdX * kShiftBwdY, kPiece = V * (int)sizeof(IO);
-    constexpr int kStages = kShiftBwdStages<IO>;
+    constexpr int kStages = shift_bwd_stages(kPiece);
     const int64_t b = blockIdx.z;
     const int64_t c = ((int64_t)blockIdx.x * kShiftBwdX + threadIdx.x) * V;
     const int64_t t0 = ((int64_t)blockIdx.y * kShiftBwdY + threadIdx.y) * p.run;
@@ -68,11 +99,12 @@ __global__ void __launch_bounds__(kShiftBwdX* kShiftBwdY, kShiftBwdCtas)
     // [stage][x, g_0 .. g_{N-1}][thread]
     __shared__ __align__(16) unsigned char ring[kRing ? kStages * (N + 1) * kThreads * kPiece : 16];
     const int tid = threadIdx.y * kShiftBwdX + threadIdx.x;
-    float acc[N][V];
+    constexpr int H = (V + 1) / 2;  // channel pairs (V == 1: the upper half idle)
+    f2 acc[N][H];
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[i][j] = 0.f;
+        for (int j = 0; j < H; ++j) acc[i][j] = 0ull;
     if (c < p.C && t0 < t1 && in_range(c + V - 1, p.C) && in_range(b, p.B)) {
         const int64_t row = b * p.T;
         const IO* x = static_cast<const IO*>(p.x);
@@ -96,76 +128,78 @@ __global__ void __launch_bounds__(kShiftBwdX* kShiftBwdY, kShiftBwdCtas)
 #pragma unroll
             for (int s = 0; s < kStages; ++s) copy_row(s);
         }
-        float m[N][V], xp[V], a[V];
+        f2 m[N][H], rest[N][H], xp[H], a[H];  // mixes, 1 - mixes
 #pragma unroll
-        for (int i = 0; i < N; ++i) load_f32<V>(p.mix[i] + c, m[i]);
+        for (int i = 0; i < N; ++i) {
+            float y[V];
+            load_f32<V>(p.mix[i] + c, y);
+            to_pairs(y, m[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) xp[j] = a[j] = 0.f;
+            for (int j = 0; j < H; ++j) rest[i][j] = fma2(m[i][j], pk(-1.f, -1.f), pk(1.f, 1.f));
+        }
+#pragma unroll
+        for (int j = 0; j < H; ++j) xp[j] = a[j] = 0ull;
         if (t0 > 0) {
-            load_vec<IO, V>(x + (row + t0 - 1) * p.C + c, xp);
+            load_pairs<IO, V>(x + (row + t0 - 1) * p.C + c, xp);
         } else if (p.x_prev) {
-            load_vec<IO, V>(static_cast<const IO*>(p.x_prev) + b * p.C + c, xp);
+            load_pairs<IO, V>(static_cast<const IO*>(p.x_prev) + b * p.C + c, xp);
         }
         IO* out = static_cast<IO*>(p.gx) + (row + t0) * p.C + c;  // row t - 1's gx goes to out - C
         int stage = 0;
 #pragma unroll(kRing ? 1 : 4)
         for (int t = 0; t < rows; ++t) {
-            float xt[V], g[N][V], own[V], prev[V];
+            f2 xt[H], g[N][H];
             if constexpr (kRing) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-                load_vec<IO, V>(reinterpret_cast<const IO*>(slot(stage, 0)), xt);
+                load_pairs<IO, V>(reinterpret_cast<const IO*>(slot(stage, 0)), xt);
 #pragma unroll
-                for (int i = 0; i < N; ++i) load_vec<IO, V>(reinterpret_cast<const IO*>(slot(stage, i + 1)), g[i]);
+                for (int i = 0; i < N; ++i) load_pairs<IO, V>(reinterpret_cast<const IO*>(slot(stage, i + 1)), g[i]);
                 copy_row(stage);
                 stage = stage + 1 == kStages ? 0 : stage + 1;
             } else {
-                load_vec<IO, V>(x + next, xt);
+                load_pairs<IO, V>(x + next, xt);
 #pragma unroll
-                for (int i = 0; i < N; ++i) load_vec<IO, V>(static_cast<const IO*>(p.g[i]) + next, g[i]);
+                for (int i = 0; i < N; ++i) load_pairs<IO, V>(static_cast<const IO*>(p.g[i]) + next, g[i]);
                 next += p.C;
             }
-            // row t's shares: own = sum m g to gx[t], prev = sum (1 - m) g to gx[t - 1]
+            // row t's share of gx[t - 1], sum (1 - m) g (of gx_prev for the first row)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                own[j] = m[0][j] * g[0][j];
-                prev[j] = fmaf(-m[0][j], g[0][j], g[0][j]);
+            for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int i = 1; i < N; ++i) {
-                    own[j] = fmaf(m[i][j], g[i][j], own[j]);
-                    prev[j] += fmaf(-m[i][j], g[i][j], g[i][j]);
-                }
-                a[j] += prev[j];
-            }
+                for (int j = 0; j < H; ++j) a[j] = fma2(rest[i][j], g[i][j], a[j]);
             if (t > 0) {
-                store_vec<IO, V>(out - p.C, a);
+                store_pairs<IO, V>(out - p.C, a);
             } else if (t0 == 0 && p.gx_prev) {
-                store_vec<IO, V>(static_cast<IO*>(p.gx_prev) + b * p.C + c, prev);
+                store_pairs<IO, V>(static_cast<IO*>(p.gx_prev) + b * p.C + c, a);
             }
             out += p.C;
             if (t < (int)(t1 - t0)) {  // (the row after the run counts in its own run)
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
+                for (int j = 0; j < H; ++j) {
+                    const f2 dx = fma2(xp[j], pk(-1.f, -1.f), xt[j]);
+                    a[j] = mul2(m[0][j], g[0][j]);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) acc[i][j] = fmaf(g[i][j], xt[j] - xp[j], acc[i][j]);
+                    for (int i = 1; i < N; ++i) a[j] = fma2(m[i][j], g[i][j], a[j]);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i][j] = fma2(g[i][j], dx, acc[i][j]);
                     xp[j] = xt[j];
-                    a[j] = own[j];
                 }
             }
         }
         if (t1 == p.T) {
             if (p.gx_last) {
-                float gl[V];
-                load_vec<IO, V>(static_cast<const IO*>(p.gx_last) + b * p.C + c, gl);
+                f2 gl[H];
+                load_pairs<IO, V>(static_cast<const IO*>(p.gx_last) + b * p.C + c, gl);
 #pragma unroll
-                for (int j = 0; j < V; ++j) a[j] += gl[j];
+                for (int j = 0; j < H; ++j) a[j] = add2(a[j], gl[j]);
             }
-            store_vec<IO, V>(out - p.C, a);
+            store_pairs<IO, V>(out - p.C, a);
         }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) red[i][threadIdx.y][j * kShiftBwdX + threadIdx.x] = acc[i][j];
+        for (int j = 0; j < V; ++j) red[i][threadIdx.y][j * kShiftBwdX + threadIdx.x] = j % 2 ? hi(acc[i][j / 2]) : lo(acc[i][j / 2]);
     __syncthreads();
     const int64_t cb = (int64_t)blockIdx.x * kShiftBwdX * V;  // the CTA's first channel
     if (p.part) {
