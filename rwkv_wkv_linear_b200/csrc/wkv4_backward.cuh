@@ -16,18 +16,18 @@
 //   gw   = sum_t e^w (P_{t+1} A_t + Q_{t+1} D_t).
 // So there are two scans, one from each end, and the second needs the first.
 //
-// Layout.  A tile is 64 channels of one batch row; a warp owns L steps (32, or
-// 16 in fp32 while T fits one round)
-// of it, a lane two adjacent channels (packed f32x2 arithmetic), a CTA NW
-// warps, a cluster of NC CTAs a round of NC NW L steps.  A round's k, v, gout
-// (and r) are copied to shared memory once and stay there:
+// Layout.  A tile is 64 channels of one batch row; a warp owns L steps of it (32,
+// or 16 in fp32, whose rows are twice as long), a lane two adjacent channels
+// (packed f32x2 arithmetic), a CTA NW warps, a cluster of NC CTAs a round of
+// NC NW L steps.  A round's k, v, gout (and r) are copied to shared memory once
+// and stay there:
 //   1. each warp summarises its chunk (a, b, p) as the forward does;
 //   2. the chunks are joined in the CTA (64 threads, a channel each), the
 //      CTAs' aggregates read through cluster shared memory;
 //   3. from the state at its start each warp walks its steps once more for
-//      y_t, al_t (kept in fp32 in shared memory, over the gout and r rows
-//      they replace), gr, and its share of gu and gw, then folds the chunk's
-//      (P, Q) from its end;
+//      y_t, al_t (kept in fp32 in tensor memory: al_t and -al_t y_t of a
+//      channel pair are four columns of the lane), gr, and its share of gu and
+//      gw, and folds the chunk's (P, Q) on the way;
 //   4. the (P, Q) are joined the same way from the other end;
 //   5. a last walk from the chunk's end writes gk, gv.
 // One round covers T when NC NW L >= T: every input is read once and every
@@ -51,9 +51,17 @@
 // R = ceil(max k log2 e), under limits like those of the forward's
 // fixed-reference path (kBwdRange, kBwdLift).  Where a limit is passed a
 // channel takes the exact per-step path (exact_backward_*: quadratic in the
-// chunk's 16 steps, fp64 exponents, any range).  gw and gu are summed in fp32:
+// chunk's steps, fp64 exponents, any range).  gw and gu are summed in fp32:
 // a thread's steps, then the warps, then (wkv4_column_sum_kernel) the CTAs, in
 // a fixed order.
+//
+// What bounds it.  B=4, T=1024, C=5120, bf16, gated: 103 us for 294 MB (2.9 TB/s)
+// and 160 warp instructions a step of 64 channels at 2.0 a clock and SM: issue,
+// with 12 warps an SM (168 registers a thread) to cover the instructions'
+// latencies, not HBM.  A fourth CTA an SM costs more in spills than it hides
+// (120 us); al, y in tensor memory instead of shared memory are what makes three
+// fit.  B=1, T=16384, C=2048, fp32, with k, v read twice: 233 us for 940 MB
+// (4.0 TB/s).  Short calls are a chain of latencies: B=1, T=48, C=768 6.4 us.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -95,7 +103,6 @@ struct BwdParams {
     uint32_t wait_rounds;  // limit of each bounded wait
     int no_push;           // checked builds' fault injection: no CTA pushes its sums
     int NC;            // CTAs a cluster
-    int nb;            // batch rows a cluster walks, one after another
     bool vec_load;     // every row of k, v, gout, r starts on 16 bytes
     bool vec_store;    // channel pairs of gk, gv, gr may be stored as one access
 };
@@ -123,6 +130,8 @@ struct BwdLayout {
     __host__ __device__ static constexpr int bytes(int NC) {
         return kPeers + NC * kBwdC * kSumBytes > kShare ? kPeers + NC * kBwdC * kSumBytes : kShare;
     }
+    // CTAs an SM that the shared memory allows, which the registers are shared by
+    static constexpr int kCtas = 3 * (bytes(8) + 1024) <= 228 * 1024 ? 3 : 2;  // an SM
     static_assert(32 * kBwdWarps * 128 >= kColumns * (65536 / 512), "registers below the columns' share");
 };
 
@@ -695,8 +704,11 @@ __device__ __forceinline__ void bwd_walk_down(const BwdChunk<IO>& ch, const BwdC
     }
 }
 
-template <typename IO, int L, bool kGate>
-__global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const BwdParams p) {
+// kOne: T fits one round.  The loop over rounds and what lives across it fall
+// away, and with them the spills at 168 registers (B=4, T=1024, C=5120, bf16,
+// gated: 95.7 us against 105.6; B=8, T=1024, C=768, fp16: 34.4 against 37.3).
+template <typename IO, int L, bool kGate, bool kOne>
+__global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas) wkv4_backward_kernel(const BwdParams p) {
     namespace cg = cooperative_groups;
     allow_dependents();
     grid_dependency_wait();
@@ -709,15 +721,14 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     const int NC = p.NC, rank = (int)cluster.block_rank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = 2 * lane;
     const int c0 = (int)blockIdx.y * kBwdC;  // grid: the cluster's CTAs, channel tiles, batch rows
-    const int T = (int)p.T, rounds = p.rounds, last = rounds - 1;
+    const int T = (int)p.T, rounds = kOne ? 1 : p.rounds, last = rounds - 1;
     const int64_t C = p.C, BC = p.B * C;
     const int round_steps = NC * Ts;
     const int64_t c = c0 + col;
     const bool ok0 = c < C, ok1 = c + 1 < C;
-    // the batch rows of this cluster, each walked from its last round to its first
-    const int b0 = blockIdx.z * p.nb, items = min(p.nb, (int)p.B - b0) * rounds;
+    const int b = blockIdx.z;
     // every global access below is (b T + t) C + c for b < B, t < T, c < C, or b C + c
-    if (!in_range(b0, p.B)) return;
+    if (!in_range(b, p.B)) return;
 
     unsigned char* const wbase = smem + warp * Lay::kWarp;
     const Sums chunk(smem + Lay::kChunks, NW * kBwdPitch);
@@ -734,8 +745,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         atomicOr(&g_device_error, kErrExchangeWait);
         failed = true;
     };
-    // an item's rows of this warp: k and v, then (a second group) gout and r
-    auto load_item = [&](int b, int round) {
+    // a round's rows of this warp: k and v, then (a second group) gout and r
+    auto load_round = [&](int round) {
         const int t0 = round * round_steps + rank * Ts + warp * L;
         const int n = chunk_steps(T, t0, L);
         const int64_t at = ((int64_t)b * T + t0) * C;
@@ -751,8 +762,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         }
         cp_async_commit();
     };
-    // an item's rows of this warp brought to L2 (32 lanes, 128 bytes each)
-    auto prefetch_item = [&](int b, int round) {
+    // a round's rows of this warp brought to L2 (32 lanes, 128 bytes each)
+    auto prefetch_round = [&](int round) {
         constexpr int kLanes = 32 / L;
         const int t = round * round_steps + rank * Ts + warp * L + lane / kLanes;
         const int cl = c0 + (lane % kLanes) * (kBwdC / kLanes);
@@ -779,7 +790,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     // Every CTA's barriers are set up before a peer's sum may arrive.  (Relaxed:
     // the barriers' own fence is enough, and a release would wait for the rows.)
     cluster_arrive_relaxed();
-    load_item(b0, last);
+    load_round(last);
     // the lane quarter of tensor memory that this warp reaches
     const uint32_t taddr = *tslot + ((uint32_t)warp << 21);
     BwdChunk<IO> ch{reinterpret_cast<const IO*>(wbase), reinterpret_cast<const IO*>(wbase + Lay::kTile),
@@ -801,27 +812,28 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
     cluster_wait_acquire();
 
     f2 gw_sum = 0ull, gu_sum = 0ull;
-    int passed = 0;  // rounds handed on so far: `after` and its barriers take turns
-
+    // the rounds from the last to the first; (P, Q) goes from turn to turn through
+    // the two rows of `after`
 #pragma unroll 1
-    for (int it = 0, b = b0, round = last; it < items; ++it) {
-        const uint32_t parity = it & 1;
-        const bool handed = round < last;  // this round goes on from the one after it
+    for (int round = last; round >= 0; --round) {
+        const int turn = last - round;
+        const uint32_t parity = turn & 1;
+        const bool handed = turn > 0;  // this round goes on from the one after it
         const int t0 = round * round_steps + rank * Ts + warp * L;
         const int n = ch.n = chunk_steps(T, t0, L);
         const int64_t at = ((int64_t)b * T + t0) * C;  // element offset of the chunk's first row
         const int64_t jch = (int64_t)b * C + c0 + jc;
-        if (it > 0) {
-            __syncwarp();  // the last item's rows have been read by every lane
-            load_item(b, round);
+        if (handed) {
+            __syncwarp();  // the last round's rows have been read by every lane
+            load_round(round);
         }
         if (threadIdx.x == 0) {  // what this round's barriers will receive
             if (rank > 0) mbar_arrive_expect_tx(bar, (uint32_t)rank * kBwdC * kSumBytes);
             if (rank < NC - 1) mbar_arrive_expect_tx(bar + 1, (uint32_t)(NC - 1 - rank) * kBwdC * kSumBytes);
-            if (rank > 0 && handed) mbar_arrive_expect_tx(bar + 2 + (passed & 1), kBwdC * kSumBytes);
+            if (rank > 0 && handed) mbar_arrive_expect_tx(bar + 2 + ((turn - 1) & 1), kBwdC * kSumBytes);
         }
-        // the next item's rows while this one is waited for
-        if (it + 1 < items) prefetch_item(round > 0 ? b : b + 1, round > 0 ? round - 1 : last);
+        // the next round's rows while this one is waited for
+        if (round > 0) prefetch_round(round - 1);
         // the state at the round's start
         Sum carry = empty_sum();
         if (jok && part == 0) {
@@ -950,8 +962,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             Sum s = empty_sum();
             if (part == P - 1) {
                 if (handed) {
-                    if (rank > 0) wait(2 + (passed & 1), (passed >> 1) & 1);
-                    s = after.get((passed & 1) * kBwdC + jc);
+                    if (rank > 0) wait(2 + ((turn - 1) & 1), ((turn - 1) >> 1) & 1);
+                    s = after.get(((turn - 1) & 1) * kBwdC + jc);
                 } else if (jok && p.gstate_out) {
                     const Sum x = sum_of(p.gstate_out[jch], p.gstate_out[BC + jch],
                                          -(double)p.state_out[2 * BC + jch] * kLog2eD);
@@ -959,7 +971,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
                     s = scaled(x.a * d.f, x.b * d.f, x.p + d.i);
                 }
             }
-            if (handed) ++passed;
             if (rank < NC - 1) wait(1, parity);
             for (int q = q1 - 1; q >= max(q0, rank + 1); --q) s = join(s, peer(q).get(jc), dT);
             s = decayed(s, d_down);
@@ -967,9 +978,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
             for (int h = 1; h < P; h *= 2) s = join(s, lane_sum<P>(s, part ^ h));
             if (rank == 0 && round > 0) {  // the round before goes on from this one's start
                 const Sum x = join(s, total, dT), y0 = scaled(x.a, x.b, x.p);
-                const int slot = (passed & 1) * kBwdC + jc;
+                const int slot = (turn & 1) * kBwdC + jc;
                 if (part == P - 1) after.put(slot, y0);
-                for (int q = 1 + part; q < NC && !p.no_push; q += P) push_sum(after, slot, y0, bar + 2 + (passed & 1), q);
+                for (int q = 1 + part; q < NC && !p.no_push; q += P) push_sum(after, slot, y0, bar + 2 + (turn & 1), q);
             }
             const Sum R1 = join(s, ex, d_after);
             chunk.put(i1, R1);
@@ -1029,13 +1040,6 @@ __global__ void __launch_bounds__(32 * kBwdWarps, 3) wkv4_backward_kernel(const 
         }
         gw_sum = add2(gw_sum, pk(gwj[0], gwj[1]));
         gu_sum = add2(gu_sum, pk(guj[0], guj[1]));
-        // the next item: the round before, then the next batch row's last
-        if (round > 0) {
-            --round;
-        } else {
-            round = last;
-            ++b;
-        }
     }
 
     // the CTA's sums of gw, gu

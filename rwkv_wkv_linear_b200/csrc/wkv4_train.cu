@@ -13,11 +13,11 @@
 namespace wkv4 {
 
 // Launch shape of the backward pass, from the sizes and the type alone (the
-// workspace is sized from it): CTAs a cluster, batch rows a cluster, rounds.
+// workspace is sized from it): steps a chunk, CTAs a cluster, rounds.
 struct BwdShape {
-    int L, NC, nb;
+    int L, NC;
     int64_t rounds;
-    int64_t rows(int64_t B) const { return (B + nb - 1) / nb * NC; }  // partial sums a channel
+    int64_t rows(int64_t B) const { return B * NC; }  // partial sums a channel
 };
 
 static BwdShape bwd_shape(int64_t B, int64_t T, int64_t C, int dtype, bool gated) {
@@ -26,33 +26,23 @@ static BwdShape bwd_shape(int64_t B, int64_t T, int64_t C, int dtype, bool gated
     auto shape = [&](int L) {
         const int64_t ctas = std::max<int64_t>(1, (T + kBwdWarps * L - 1) / (kBwdWarps * L));
         s.L = L;
-        // 8 CTAs a cluster at most, 16 where the clusters are few: a round is then
-        // a chain of latencies, and there are half as many.  No more of them
-        // than the rounds need: a CTA without steps keeps its place all the same.
-        const int most = tiles * kBwdMaxCtas <= 2 * 148 ? kBwdMaxCtas : 8;
+        // 8 CTAs a cluster at most, 16 where all of them fit the GPU at once or in
+        // two waves of 3 an SM with one round: a round is a chain of latencies,
+        // and the second makes k, v be read twice, but what wide clusters wait
+        // for each other grows with their number.  bf16, gated, with 8 and 16:
+        // B=1, T=2048, C=768 37.0, 16.3 us; B=4, T=2048, C=768 54.4, 49.2; B=4,
+        // T=1536, C=2560 97.3, 100.4; B=4, T=2048, C=5120 241, 261.  No more of
+        // them than the rounds need: a CTA without steps keeps its place all the same.
+        const bool wide = tiles * kBwdMaxCtas <= 2 * 148 || (ctas <= kBwdMaxCtas && tiles * ctas <= 6 * 148);
+        const int most = wide ? kBwdMaxCtas : 8;
         s.rounds = (ctas + most - 1) / most;
         s.NC = (int)((ctas + s.rounds - 1) / s.rounds);
     };
     // Steps a chunk: 32; in fp32 (twice the shared memory, so fewer CTAs an SM)
     // 16 unless the CTAs are few and walk several rounds, whose joins are then
-    // spread over twice the steps (B=1, T=16384, C=2048: 322 us with 16, 231 with 32).
+    // spread over twice the steps (B=1, T=16384, C=2048: 346 us with 16, 233 with 32).
     shape(dtype == WKV4_F32 ? 16 : 32);
     if (dtype == WKV4_F32 && !gated && s.rounds > 1 && tiles * s.NC <= 2 * 148) shape(32);
-    // Batch rows a cluster walks one after another, its set-up (constants,
-    // barriers, tensor memory) paid once for all of them: the most, up to 4,
-    // that do not lengthen the waves of CTAs (3 an SM) times the rows each
-    // walks.  Measured (bf16, gated): B=4, T=1024, C=5120 113.3 us with 2,
-    // 116.0 with 1, 118.3 with 4; B=8, T=1024, C=768 (fp16) 39.7, 41.9, 53.2.
-    int64_t best = INT64_MAX;
-    s.nb = 1;
-    for (int nb = 1; nb <= 4 && nb <= B; ++nb) {
-        const int64_t grid = (C + kBwdC - 1) / kBwdC * s.NC * ((B + nb - 1) / nb);
-        const int64_t cost = (grid + 3 * 148 - 1) / (3 * 148) * nb;
-        if (cost <= best) {
-            best = cost;
-            s.nb = nb;
-        }
-    }
     return s;
 }
 
@@ -79,10 +69,10 @@ static cudaError_t launch_column_sum(const float* part, float* o0, float* o1, fl
                       dim3(256), 0, stream, p);
 }
 
-template <typename IO, int L, bool kGate>
+template <typename IO, int L, bool kGate, bool kOne>
 static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdShape& sh) {
     using Lay = BwdLayout<IO, L, kGate>;
-    auto kern = wkv4_backward_kernel<IO, L, kGate>;
+    auto kern = wkv4_backward_kernel<IO, L, kGate, kOne>;
     static DeviceFlags attr;
     cudaError_t e = ensure_smem_attr(attr, kern, Lay::bytes(kBwdMaxCtas));
     if (e != cudaSuccess) return e;
@@ -92,7 +82,7 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
         if (e != cudaSuccess) return e;
     }
     const unsigned tiles = (unsigned)((a.C + kBwdC - 1) / kBwdC), threads = 32 * kBwdWarps;
-    if (sh.rounds > 1) {
+    if constexpr (!kOne) {
         auto sum = wkv4_backward_summary_kernel<IO, L>;
         const size_t smem = kBwdWarps * (4 * Lay::kTile + kBwdC * kSumBytes);
         static DeviceFlags sattr;
@@ -108,7 +98,7 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
     }
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
-    cfg.gridDim = launch_grid(dim3((unsigned)sh.NC, tiles, (unsigned)(sh.rows(a.B) / sh.NC)));
+    cfg.gridDim = launch_grid(dim3((unsigned)sh.NC, tiles, (unsigned)a.B));
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = Lay::bytes(sh.NC);
     cfg.stream = a.stream;
@@ -128,13 +118,19 @@ static cudaError_t launch_backward_t(const BwdArgs& a, BwdParams& p, const BwdSh
     return e;
 }
 
+template <typename IO, int L, bool kGate>
+static cudaError_t launch_backward_rounds(const BwdArgs& a, BwdParams& p, const BwdShape& sh) {
+    return sh.rounds == 1 ? launch_backward_t<IO, L, kGate, true>(a, p, sh)
+                          : launch_backward_t<IO, L, kGate, false>(a, p, sh);
+}
+
 template <typename IO>
 static cudaError_t launch_backward_io(const BwdArgs& a, BwdParams& p, const BwdShape& sh) {
     if constexpr (sizeof(IO) == 4) {
-        if (sh.L == 32) return launch_backward_t<IO, 32, false>(a, p, sh);
-        return a.r ? launch_backward_t<IO, 16, true>(a, p, sh) : launch_backward_t<IO, 16, false>(a, p, sh);
+        if (sh.L == 32) return launch_backward_rounds<IO, 32, false>(a, p, sh);
+        return a.r ? launch_backward_rounds<IO, 16, true>(a, p, sh) : launch_backward_rounds<IO, 16, false>(a, p, sh);
     } else {
-        return a.r ? launch_backward_t<IO, 32, true>(a, p, sh) : launch_backward_t<IO, 32, false>(a, p, sh);
+        return a.r ? launch_backward_rounds<IO, 32, true>(a, p, sh) : launch_backward_rounds<IO, 32, false>(a, p, sh);
     }
 }
 
@@ -175,7 +171,6 @@ cudaError_t launch_backward(const BwdArgs& a) {
     }
     const size_t es = dtype_size(a.dtype);
     p.NC = sh.NC;
-    p.nb = sh.nb;
     p.vec_load = (a.C * es) % 16 == 0 && aligned(a.k, 16) && aligned(a.v, 16) && aligned(a.gy, 16) &&
                  aligned(a.r, 16);
     p.vec_store = a.C % 2 == 0 && aligned(a.gk, 2 * es) && aligned(a.gv, 2 * es) && aligned(a.gr, 2 * es);
