@@ -1,5 +1,6 @@
 /*
- * wkv4.h -- C ABI of the RWKV-4 WKV forward and decode step on NVIDIA B200 (sm_100a).
+ * wkv4.h -- C ABI of the RWKV-4 WKV recurrence on NVIDIA B200 (sm_100a): forward,
+ * decode step, backward pass, token shift, and beam search over a state pool.
  *
  * The operation (per batch row b and channel c, independently):
  *   with decay w = w_c (normally -exp(time_decay_c)) and bonus u = u_c,

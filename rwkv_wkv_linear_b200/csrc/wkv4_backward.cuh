@@ -55,13 +55,13 @@
 // a thread's steps, then the warps, then (wkv4_column_sum_kernel) the CTAs, in
 // a fixed order.
 //
-// What bounds it.  B=4, T=1024, C=5120, bf16, gated: 103 us for 294 MB (2.9 TB/s)
-// and 160 warp instructions a step of 64 channels at 2.0 a clock and SM: issue,
-// with 12 warps an SM (168 registers a thread) to cover the instructions'
-// latencies, not HBM.  A fourth CTA an SM costs more in spills than it hides
-// (120 us); al, y in tensor memory instead of shared memory are what makes three
-// fit.  B=1, T=16384, C=2048, fp32, with k, v read twice: 233 us for 940 MB
-// (4.0 TB/s).  Short calls are a chain of latencies: B=1, T=48, C=768 6.4 us.
+// What bounds it.  B=4, T=1024, C=5120, bf16, gated: 95.8 us for 294 MB (3.1 TB/s)
+// and 159 warp instructions a step of 64 channels at 2.2 a clock and SM: issue,
+// with 12 warps an SM (by shared memory and registers alike) to cover the
+// instructions' latencies, not HBM.  A fourth CTA an SM costs more in spills
+// than it hides; al, y in tensor memory instead of shared memory are what makes
+// three fit.  B=1, T=16384, C=2048, fp32, with k, v read twice: 227 us for 940 MB
+// (4.1 TB/s).  Short calls are a chain of latencies: B=1, T=48, C=768 5.6 us.
 #pragma once
 
 #include <cooperative_groups.h>

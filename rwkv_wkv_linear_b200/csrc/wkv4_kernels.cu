@@ -7,7 +7,7 @@
 // ("RWKV in a self-built engine: a second non-attention paradigm (WKV/RNN)",
 // Methods table "Precision"; Reproducibility / Provenance "Implementation").
 //
-// Kernels (one translation unit, so they share the device error word):
+// Kernels (the backward passes are in wkv4_train.cu, beam search in wkv4_beam.cu):
 //   wkv4_scan_kernel    (wkv4_scan.cuh) chunked scan, time segments chained
 //                       through a thread-block cluster; TMA in, TMA out (one
 //                       round) or stores from registers (several rounds).

@@ -5,10 +5,10 @@ A gradient is a sum of terms computed in fp32 and rounded once to its type:
 with mag the sum of the terms' magnitudes (oracle/backward.py) and K the
 roundings a term can meet, in units of 2^-24 (one fp32 rounding is half of
 2^-23):
-  * a chunk's Horner walk: 16 steps of 2 roundings;
-  * the joins of chunks (8 a CTA), CTAs (8 a cluster) and rounds: each an
-    ex2.approx (2 ulp: 4), the rounding of its fp32 argument (1) and a product
-    and a sum (2);
+  * a chunk's Horner walk: up to 32 steps of 2 roundings;
+  * the joins of chunks (4 a CTA), CTAs (up to 16 a cluster) and rounds: each a
+    decay rounded (1), a product and a sum (2), powers of two being exact; in
+    all 64 + 3 (20 + rounds), which 2 16 + 7 (16 + rounds) below bounds;
   * this twice over in the forward's sums (numerator and denominator of one
     quotient) and once more in (P, Q): three passes, plus 16 for the
     exponentials, reciprocals and products of the step itself (two ex2, two
@@ -21,7 +21,7 @@ meets on its way to a gradient of one step are a gradient |g| <= 6 and
 |v| + |y| <= 12 (standard normal draws), in at most three terms:
 3 72 2^-126 < 2^-118; a sum over n steps n times that (`terms`).
 gw, gu, gmix: the magnitudes' sum again, plus the additions a term goes
-through (16 steps, a round each, 8 warps, then the rows a group of 8 adds).
+through (32 steps, a round each, 4 warps, then the rows a group of 8 adds).
 """
 
 import numpy as np
