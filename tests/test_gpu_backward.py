@@ -128,6 +128,20 @@ def test_gradients_outside_the_usual_range(cuda_device, kind, dt):
                         terms=B * T)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,masked", [(5, (4, 5)), (40, (0, 3)), (40, (30, 40)), (200, (150, 200)), (300, (32, 64)),
+                                      (2200, (2000, 2200))], ids=str)
+def test_gradients_of_masked_steps(cuda_device, T, masked, dt):
+    """Keys of -inf (padded steps): they weigh nothing and get no gradient, in
+    part of a chunk, in whole chunks and in whole CTAs, at either end."""
+    x = _inputs(2, T, 70, dt, seed=T + masked[0], gated=True, state=True)
+    x["k"][:, masked[0]:masked[1]] = -float("inf")
+    g, s = _run(x, cuda_device)
+    with np.errstate(all="ignore"):
+        _check(x, g, s, dt, f"masked {masked} of {T} {dt}")
+    assert not g.gk[:, masked[0]:masked[1]].any()
+
+
 @pytest.mark.parametrize("dt,off", [("f32", 1), ("bf16", 1), ("f16", 4)])
 def test_gradients_of_misaligned_rows(cuda_device, dt, off):
     """Bases off the 16-byte grid: loads and stores element by element, the
