@@ -317,6 +317,27 @@ def test_token_shift_gradients_match_oracle(cuda_device, shape, outs, carry, dt)
         gradcheck.check(got.cpu(), ref["gmix"][i], mag["gmix"][i], "f32", K, f"gmix {i}")
 
 
+@pytest.mark.parametrize("dt,off", [("bf16", 4), ("f16", 1), ("f32", 2)])
+def test_token_shift_gradients_of_unaligned_rows(cuda_device, dt, off):
+    """One tensor `off` elements past 16 bytes: fewer channels a thread, the same gradients."""
+    B, T, C = 37, 700, 16
+    g = torch.Generator().manual_seed(off)
+    x, gk, gv = (torch.randn(B, T, C, generator=g).to(DT[dt]) for _ in range(3))
+    mk, mv = torch.rand(C, generator=g), torch.rand(C, generator=g)
+    buf = torch.empty(B * T * C + off, dtype=DT[dt], device=cuda_device)
+    xd = buf[off:].view(B, T, C)
+    xd.copy_(x)
+    dv = lambda t: t.to(cuda_device)
+    out = wkv4.token_shift_backward(xd, dv(mk), dv(mv), dv(gk), dv(gv))
+    torch.cuda.synchronize()
+    ref, mag = ob.token_shift_backward(x, [mk, mv], [gk, gv])
+    gradcheck.check(out.gx.cpu(), ref["gx"], mag["gx"], dt, 8, "gx")
+    blocks = max(1, 148 * 8 // B)
+    K = 4 + max(8, -(-T // blocks)) + 4 + B * blocks / 8 + 8
+    for i, got in enumerate([out.gmix_k, out.gmix_v]):
+        gradcheck.check(got.cpu(), ref["gmix"][i], mag["gmix"][i], "f32", K, f"gmix {i}")
+
+
 def test_token_shift_gradients_of_zero_steps(cuda_device):
     B, C = 2, 24
     x = torch.empty(B, 0, C, device=cuda_device)
