@@ -94,7 +94,7 @@ struct BwdParams {
     void* gv;
     void* gr;
     float* gstate_in;  // [3][B][C] or NULL
-    float* part_w;     // [rows][C] partial sums, row (grid y) NC + rank
+    float* part_w;     // [rows][C] partial sums, row b NC + rank
     float* part_u;
     // rounds > 1: per round and channel the summary, then the state at the round's start
     int* ck_p;         // [rounds][B C]
