@@ -781,14 +781,16 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
     const float jw = jok ? __ldg(p.w + c0 + jc) : 0.f;
     BwdConsts cc;
     cc.load(p.w, p.u, c, C);
-    if (threadIdx.x < 4) mbar_init(bar + threadIdx.x, 1);
-    if (threadIdx.x == 0) fence_mbar_init();
+    if (threadIdx.x < 4) {  // each thread fences the barrier it has set up
+        mbar_init(bar + threadIdx.x, 1);
+        fence_mbar_init();
+    }
     if (warp == 0) tmem_alloc(tslot, Lay::kColumns);
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
     // Every CTA's barriers are set up before a peer's sum may arrive.  (Relaxed:
-    // the barriers' own fence is enough, and a release would wait for the rows.)
+    // each barrier has its own fence, and a release would wait for the rows.)
     cluster_arrive_relaxed();
     load_round(last);
     // the lane quarter of tensor memory that this warp reaches
