@@ -77,6 +77,7 @@ constexpr int kBwdWarps = 4;    // warps a CTA
 constexpr int kBwdMaxCtas = 16;  // CTAs a cluster
 constexpr int kBwdPitch = 68;   // sums a row of the chunks' (2 lanes a channel, 2 chunks each, meet no bank twice)
 constexpr int kSumBytes = 12;   // a sum in memory: p, a, b
+constexpr int kMuteNone = -1, kMuteAll = -2;
 
 struct BwdParams {
     int64_t B, T, C;
@@ -101,7 +102,7 @@ struct BwdParams {
     float* ck_a;
     float* ck_b;
     uint32_t wait_rounds;  // limit of each bounded wait
-    int no_push;           // checked builds' fault injection: no CTA pushes its sums
+    int mute;              // checked builds' fault injection: the rank that pushes no sums, kMuteNone or kMuteAll
     int NC;            // CTAs a cluster
     bool vec_load;     // every row of k, v, gout, r starts on 16 bytes
     bool vec_store;    // channel pairs of gk, gv, gr may be stored as one access
@@ -738,13 +739,19 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
     // barriers: the lower ranks' forward sums, the higher ranks' (P, Q), the two rows of `after`
     uint64_t* const bar = reinterpret_cast<uint64_t*>(smem + Lay::kBars);
     uint32_t* const tslot = reinterpret_cast<uint32_t*>(bar + 4);
-
-    bool failed = false;  // a bounded wait ran out: go on without waiting (the results are reported bad)
+    // A bounded wait that runs out sets the CTA's flag and the error word: from then
+    // on the CTA waits for, arms and pushes nothing (its results are reported
+    // bad), and stays until the cluster's other CTAs are done, whose sums may
+    // still be on their way to it.
+    volatile int* const s_fail = reinterpret_cast<volatile int*>(tslot + 1);
+    bool failed = false;  // as this thread knows it
     auto wait = [&](int which, uint32_t parity) {
         if (failed || mbar_wait_cluster_bounded(bar + which, parity, p.wait_rounds)) return;
         atomicOr(&g_device_error, kErrExchangeWait);
         failed = true;
+        *s_fail = 1;
     };
+    const bool muted = p.mute == rank || p.mute == kMuteAll;
     // a round's rows of this warp: k and v, then (a second group) gout and r
     auto load_round = [&](int round) {
         const int t0 = round * round_steps + rank * Ts + warp * L;
@@ -785,6 +792,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
         mbar_init(bar + threadIdx.x, 1);
         fence_mbar_init();
     }
+    if (threadIdx.x == 0) *s_fail = 0;
     if (warp == 0) tmem_alloc(tslot, Lay::kColumns);
     tmem_fence_before_sync();
     __syncthreads();
@@ -828,8 +836,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
         if (handed) {
             __syncwarp();  // the last round's rows have been read by every lane
             load_round(round);
+            failed |= *s_fail != 0;  // (no thread waits between the last round's end and this one's first barrier)
         }
-        if (threadIdx.x == 0) {  // what this round's barriers will receive
+        if (threadIdx.x == 0 && !failed) {  // what this round's barriers will receive
             if (rank > 0) mbar_arrive_expect_tx(bar, (uint32_t)rank * kBwdC * kSumBytes);
             if (rank < NC - 1) mbar_arrive_expect_tx(bar + 1, (uint32_t)(NC - 1 - rank) * kBwdC * kSumBytes);
             if (rank > 0 && handed) mbar_arrive_expect_tx(bar + 2 + ((turn - 1) & 1), kBwdC * kSumBytes);
@@ -874,7 +883,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
             const Sum total = lane_sum<P>(y, P - 1);
             Sum ex = lane_sum<P>(y, part - 1);
             if (part == 0) ex = empty_sum();
-            for (int q = rank + 1 + part; q < NC && !p.no_push; q += P) push_sum(peer(rank), jc, total, bar, q);
+            for (int q = rank + 1 + part; q < NC && !muted && !failed; q += P)
+                push_sum(peer(rank), jc, total, bar, q);
             Sum s = carry;  // part 0: the round's start; the others: empty
             if (rank > 0) {
                 wait(0, parity);
@@ -957,7 +967,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
             const Sum total = lane_sum<P>(y, 0);
             Sum ex = lane_sum<P>(y, part + 1);
             if (part == P - 1) ex = empty_sum();
-            for (int q = rank - 1 - part; q >= 0 && !p.no_push; q -= P) push_sum(peer(rank), jc, total, bar + 1, q);
+            failed |= *s_fail != 0;
+            for (int q = rank - 1 - part; q >= 0 && !muted && !failed; q -= P)
+                push_sum(peer(rank), jc, total, bar + 1, q);
             // (P, Q) after the round: what rank 0 found last round, or the last
             // state's, carried on to the end of the last round (as if the
             // recurrence ran on there: every chunk is a whole one to the joins)
@@ -982,7 +994,8 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
                 const Sum x = join(s, total, dT), y0 = scaled(x.a, x.b, x.p);
                 const int slot = (turn & 1) * kBwdC + jc;
                 if (part == P - 1) after.put(slot, y0);
-                for (int q = 1 + part; q < NC && !p.no_push; q += P) push_sum(after, slot, y0, bar + 2 + (turn & 1), q);
+                for (int q = 1 + part; q < NC && !muted && !failed; q += P)
+                    push_sum(after, slot, y0, bar + 2 + (turn & 1), q);
             }
             const Sum R1 = join(s, ex, d_after);
             chunk.put(i1, R1);
@@ -1051,7 +1064,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
     float* const red = reinterpret_cast<float*>(smem);  // [2][NW][64], over the rows
     *reinterpret_cast<f2*>(red + warp * kBwdC + col) = gw_sum;
     *reinterpret_cast<f2*>(red + (NW + warp) * kBwdC + col) = gu_sum;
-    __syncthreads();
+    const bool gave_up = __syncthreads_or(failed);
     for (int i = threadIdx.x; i < 2 * kBwdC; i += 32 * NW) {
         const int which = i / kBwdC, ci = i % kBwdC;
         if (c0 + ci < C) {
@@ -1063,7 +1076,13 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
     }
     // (the barriers above are behind every warp's last access to tensor memory)
     if (warp == 0) tmem_dealloc(*tslot, Lay::kColumns);
-    // every sum pushed to this CTA has been waited for, so it may leave
+    // Every sum pushed to this CTA has been waited for, so it may leave -- unless
+    // it gave up: then it leaves behind the others (a CTA that exits counts as
+    // arrived, and each does, its waits being bounded).
+    if (gave_up) {
+        cluster_arrive_relaxed();
+        cluster_wait_acquire();
+    }
 }
 
 // Summary of every round's k, v (several rounds): CTA (tile, round), each

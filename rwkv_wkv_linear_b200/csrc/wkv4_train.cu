@@ -175,7 +175,11 @@ cudaError_t launch_backward(const BwdArgs& a) {
                  aligned(a.r, 16);
     p.vec_store = a.C % 2 == 0 && aligned(a.gk, 2 * es) && aligned(a.gv, 2 * es) && aligned(a.gr, 2 * es);
     p.wait_rounds = wait_rounds();
-    p.no_push = fault_plan().exchange ? 1 : 0;
+    p.mute = kMuteNone;
+#ifdef WKV4_CHECKED
+    // with WKV4_FAULT_RANK=R the injected fault silences the CTAs of rank R alone
+    if (fault_plan().exchange) p.mute = env_int("WKV4_FAULT_RANK", kMuteAll);
+#endif
     if (a.T == 0) {
         const int64_t n = a.B * a.C;
         return launch_pdl(wkv4_backward_no_steps_kernel, launch_grid(dim3((unsigned)((n + 127) / 128))),
