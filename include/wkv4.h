@@ -323,6 +323,11 @@ WKV4_API size_t wkv4_forward_host_workspace(int64_t B, int64_t T, int64_t C, int
  *   workspace   device memory of at least wkv4_backward_workspace(B, T, C,
  *               dtype) bytes, 16-byte aligned (may be NULL where that is 0),
  *               for this call alone until the stream has passed it.
+ * Keys may be masks of any finite size (-1e9, -1e30), with usual ones before
+ * them or none.  Keys and state maxima past 1.02e9 nats in magnitude count as
+ * that, and from 7.8e14 (2^50 / log2 e) on as one value further out, next to
+ * which a decay or a bonus is lost (as beside a max of 1e17 in fp64): only
+ * steps that have nothing but such keys before them can tell.
  * No output may overlap an input, the workspace or another output:
  * WKV4_ERR_ALIAS.  T == 0: gstate_in <- gstate_out's share (the state passes
  * through), gw = gu = 0.  B == 0 or C == 0: nothing is written but gw and gu

@@ -46,14 +46,23 @@
 // Numerics.  Sums are carried as (a, b, p): A = a 2^p, D = b 2^p with an integer
 // p, so that joins scale by exact powers of two and no exponential or fp64
 // enters them; the decay over n steps is a factor in (1/2, 1] and an integer
-// exponent, worked out in fp64 once a thread.  (P, Q) is carried the same way.
+// exponent, worked out once a thread.  (P, Q) is carried the same way.
 // Within a chunk everything is held against the chunk's reference 2^R,
 // R = ceil(max k log2 e), under limits like those of the forward's
 // fixed-reference path (kBwdRange, kBwdLift).  Where a limit is passed a
 // channel takes the exact per-step path (exact_backward_*: quadratic in the
-// chunk's steps, fp64 exponents, any range).  gw and gu are summed in fp32:
-// a thread's steps, then the warps, then (wkv4_column_sum_kernel) the CTAs, in
-// a fixed order.
+// chunk's steps, fp64 exponents).
+//
+// Masks.  Where no usual key came yet, a state is made of the keys that stand
+// for a mask (-1e9, -1e30) alone, so their exponents count too, and they do not
+// all fit 32 bits.  Exponents up to +-kNear (1.02e9 nats) are held as they are;
+// keys and maxima beyond count as kNear, and from 2^50 on as one value further
+// out, kStill, that a decay does not move: next to a max that large a decay is
+// lost in the forward's fp64 as well.  So two steps' weights are told apart
+// unless both keys lie past 1.02e9 nats on the same side of 2^50.
+//
+// gw and gu are summed in fp32: a thread's steps, then the warps, then
+// (wkv4_column_sum_kernel) the CTAs, in a fixed order.
 //
 // What bounds it.  B=4, T=1024, C=5120, bf16, gated: 95.8 us for 294 MB (3.1 TB/s)
 // and 159 warp instructions a step of 64 channels at 2.2 a clock and SM: issue,
@@ -141,7 +150,14 @@ struct BwdLayout {
 // or the (P, Q) behind it may lie above the reference, in powers of two.
 constexpr float kBwdRange = 40.f;
 constexpr int kBwdLift = 63;
-constexpr int kNone = -(1 << 30);  // exponent of an empty sum
+// Exponents (log2 units).  Decays carry one on by 2^20 in a chunk and 1.1e8 in a
+// round, after which it is brought back to kReach.
+constexpr int kNear = 1480000000;
+constexpr int kReach = 1520000000;
+constexpr int kStillFrom = 1650000000;  // from here on (in magnitude) a decay does not move it:
+constexpr int kStill = 1700000000;      // exponents of 2^50 and more
+constexpr int kNone = -1950000000;      // an empty sum's, below every other
+constexpr double kStillD = 0x1p100;     // kStill as an fp64 exponent, which swallows decays by itself
 
 // A = a 2^p, D = b 2^p.
 struct Sum {
@@ -157,14 +173,30 @@ struct Decay {
 __device__ __forceinline__ Sum empty_sum() { return {0.f, 0.f, kNone}; }
 // 2^d, 0 below the normal range, d <= 127
 __device__ __forceinline__ float pow2i(int d) { return __int_as_float(max(d + 127, 0) << 23); }
+// 2^{low - high} (the distance may take all 32 bits)
+__device__ __forceinline__ float pow2_below(int low, int high) {
+    // bits of 1.0 less the distance in the exponent's place, as one multiply-add (B=4, T=1024, C=5120
+    // 95.0 us against 95.5 with a shift and a subtraction)
+    int r;
+    asm("mad.lo.s32 %0, %1, -8388608, 1065353216;" : "=r"(r) : "r"((int)min((unsigned)high - (unsigned)low, 127u)));
+    return __int_as_float(r);
+}
+__device__ __forceinline__ bool is_still(int p) { return abs(p) >= kStillFrom; }
+// The exponent of a key or of a state's max.
+__device__ __forceinline__ double key2(float k) {
+    const double x = (double)k * kLog2eD;
+    if (!(fabs(x) > (double)kNear) || isinf(k)) return x;
+    return copysign(fabs(x) < 0x1p50 ? (double)kNear : kStillD, x);
+}
 // w in log2 units as two floats.  Decays faster than 2^-32768 a step are taken
-// as that: nothing passes either, and n steps of it stay an integer exponent.
+// as that: nothing passes either, and n steps of it stay an integer exponent
+// (likewise growth above 2^32768).
 struct Rate {
     float hi, lo;
 };
 __device__ __forceinline__ Rate rate_of(float w) {
     const float hi = w * kLog2e;
-    if (!(hi >= -32768.f)) return {-32768.f, 0.f};
+    if (!(fabsf(hi) <= 32768.f)) return {hi > 0.f ? 32768.f : -32768.f, 0.f};
     constexpr float kLog2eLo = (float)(kLog2eD - (double)kLog2e);
     return {hi, fmaf(w, kLog2e, -hi) + w * kLog2eLo};
 }
@@ -176,26 +208,40 @@ __device__ __forceinline__ Decay decay_of(Rate r, int n) {
     // grows with the number of chunks a slow decay remembers)
     return {exp2f((x - c) + (fmaf((float)n, r.hi, -x) + (float)n * r.lo)), (int)c};
 }
-__device__ __forceinline__ Sum decayed(Sum x, Decay d) { return {x.a * d.f, x.b * d.f, x.p + d.i}; }
+__device__ __forceinline__ Sum decayed(Sum x, Decay d) {
+    const bool still = is_still(x.p);
+    const float f = still ? 1.f : d.f;
+    return {x.a * f, x.b * f, still ? x.p : x.p + d.i};
+}
 // a 2^p, b 2^p with a fractional p
 __device__ __forceinline__ Sum sum_of(float a, float b, double p) {
-    const double c = ceil(fmin(fmax(p, -5e8), 5e8));
-    const float f = exp2f((float)fmax(p - c, -200.0));
+    if (a == 0.f && b == 0.f) return empty_sum();
+    if (fabs(p) >= (double)kStillFrom) {
+        if (p <= -INFINITY) return empty_sum();
+        return {a, b, p < 0.0 ? -kStill : kStill};
+    }
+    const double c = p == p ? ceil(p) : 0.0;  // (a NaN goes on in a and b)
+    const float f = exp2f((float)(p - c));
     return {a * f, b * f, (int)c};
 }
-__device__ __forceinline__ St st_of(Sum x) { return {x.a, x.b, (double)x.p}; }
+__device__ __forceinline__ double exponent_of(int p) {
+    if (!is_still(p)) return (double)p;
+    return p > 0 ? kStillD : p >= -kStill ? -kStillD : kEmptyMax2;
+}
+__device__ __forceinline__ St st_of(Sum x) { return {x.a, x.b, exponent_of(x.p)}; }
 
 // x, decayed by d, and y added.
 __device__ __forceinline__ Sum join(Sum x, Sum y, Decay d) {
-    const int px = x.p + d.i, p = max(px, y.p);
-    const float fx = pow2i(px - p) * d.f, fy = pow2i(y.p - p);
+    const bool still = is_still(x.p);
+    const int px = still ? x.p : x.p + d.i, p = max(px, y.p);
+    const float fx = pow2_below(px, p) * (still ? 1.f : d.f), fy = pow2_below(y.p, p);
     return {fmaf(x.a, fx, y.a * fy), fmaf(x.b, fx, y.b * fy), p};
 }
 
 // x and y added.
 __device__ __forceinline__ Sum join(Sum x, Sum y) {
     const int p = max(x.p, y.p);
-    const float fx = pow2i(x.p - p), fy = pow2i(y.p - p);
+    const float fx = pow2_below(x.p, p), fy = pow2_below(y.p, p);
     return {fmaf(x.a, fx, y.a * fy), fmaf(x.b, fx, y.b * fy), p};
 }
 
@@ -206,14 +252,14 @@ __device__ __forceinline__ Sum lane_sum(Sum x, int from) {
             __shfl_sync(0xffffffffu, x.p, from, P)};
 }
 
-// The larger magnitude brought to [1, 2).
+// The larger magnitude brought to [1, 2), and an exponent that decays have
+// carried past kReach back to it.
 __device__ __forceinline__ Sum scaled(float a, float b, int p) {
-    const float m = fmaxf(fabsf(a), fabsf(b));
-    const int e = (__float_as_int(m) >> 23) & 0xff;
-    if (m == 0.f) return empty_sum();
-    if (e == 0 || e == 255) return {a, b, p};  // subnormal, or infinite / NaN: as it is
+    const int e = (__float_as_int(fmaxf(fabsf(a), fabsf(b))) >> 23) & 0xff;
+    if (e == 0 || e == 255 || is_still(p))  // zero, subnormal, infinite or NaN: as it is
+        return a == 0.f && b == 0.f ? empty_sum() : Sum{a, b, p};
     const float s = __int_as_float((254 - e) << 23);
-    return {a * s, b * s, p + e - 127};
+    return {a * s, b * s, min(max(p + e - 127, -kReach), kReach)};
 }
 
 // [n] sums in shared memory: p, then a, then b
@@ -326,10 +372,12 @@ __device__ __forceinline__ void load_rows(unsigned char* dst, const IO* const (&
     }
 }
 
-// The same with an fp64 exponent, for the exact paths.
+// The same with an fp64 exponent, for the exact paths.  (One that swallows decays
+// would swallow the change of scale.)
 __device__ __forceinline__ St scaled_st(float P, float Q, double p) {
     const Sum x = scaled(P, Q, 0);
-    return x.p == kNone ? empty_state() : St{x.a, x.b, p + (double)x.p};
+    if (x.p == kNone) return empty_state();
+    return fabs(p) >= (double)kStillFrom ? St{P, Q, p} : St{x.a, x.b, p + (double)x.p};
 }
 
 // Gradients through the gate: g = s gout and, through the pointer, gr.
@@ -367,14 +415,31 @@ __device__ __forceinline__ ExactOut exact_out(const St& s, double x, float v, do
     return {fmaf(f1, s.a, f2 * v) * rz, rz, f2, q};
 }
 
+// The state after a step of exponent x.
+__device__ __forceinline__ void exact_advance(St& s, double x, float v, double w2) {
+    const double q = fmax(s.p + w2, x);
+    const float f1 = ex2((float)(s.p + w2 - q)), f2 = ex2((float)(x - q));
+    s.a = fmaf(f1, s.a, f2 * v);
+    s.b = fmaf(f1, s.b, f2);
+    s.p = q;
+}
+// A chunk's sums from the empty state, rows in shared memory.
+template <typename IO>
+__device__ __noinline__ St exact_summary(const IO* sk, const IO* sv, int n, double w2) {
+    St s = empty_state();
+    for (int i = 0; i < n; ++i) exact_advance(s, key2(Io<IO>::to_f(sk[i * kBwdC])), Io<IO>::to_f(sv[i * kBwdC]), w2);
+    return s;
+}
+
 // Upward walk: gr, and the chunk's (P, Q) at its start from zero at its end.
 template <typename IO>
 __device__ __noinline__ St exact_backward_up(const ExactChunk<IO> c, IO* gr_out) {
     St s = c.S, acc = empty_state();
     for (int i = 0; i < c.n; ++i) {
         const int64_t o = (int64_t)i * c.stride;
-        const float k = Io<IO>::to_f(c.k[o]), v = Io<IO>::to_f(c.v[o]);
-        const ExactOut e = exact_out(s, (double)k * kLog2eD, v, c.u2);
+        const double x = key2(Io<IO>::to_f(c.k[o]));
+        const float v = Io<IO>::to_f(c.v[o]);
+        const ExactOut e = exact_out(s, x, v, c.u2);
         float g = Io<IO>::to_f(c.gy[o]);
         if (c.r) {
             float gr;
@@ -383,7 +448,7 @@ __device__ __noinline__ St exact_backward_up(const ExactChunk<IO> c, IO* gr_out)
         }
         const float al = g * e.rz;
         acc = combine(acc, scaled_st(al, -al * e.y, (double)i * c.w2 - e.q), 0.0);
-        exact_update(s, k, v, c.w2);
+        exact_advance(s, x, v, c.w2);
     }
     return scaled_st(acc.a, acc.b, acc.p);
 }
@@ -403,11 +468,11 @@ __device__ __noinline__ ExactGrads exact_backward_down(const ExactChunk<IO> c, S
         St s = c.S;
         for (int j = 0; j < i; ++j) {
             const int64_t o = (int64_t)j * c.stride;
-            exact_update(s, Io<IO>::to_f(c.k[o]), Io<IO>::to_f(c.v[o]), c.w2);
+            exact_advance(s, key2(Io<IO>::to_f(c.k[o])), Io<IO>::to_f(c.v[o]), c.w2);
         }
         const int64_t o = (int64_t)i * c.stride;
-        const float k = Io<IO>::to_f(c.k[o]), v = Io<IO>::to_f(c.v[o]);
-        const double x = (double)k * kLog2eD;
+        const float v = Io<IO>::to_f(c.v[o]);
+        const double x = key2(Io<IO>::to_f(c.k[o]));
         const ExactOut e = exact_out(s, x, v, c.u2);
         float g = Io<IO>::to_f(c.gy[o]);
         if (c.r) {
@@ -557,7 +622,7 @@ __device__ __forceinline__ void bwd_summary(const IO* sk, const IO* sv, int col,
             const float s = __int_as_float((254 - e) << 23);
             sum[j] = {Aj[j] * s, Dj[j] * s, (int)ref.R[j] + e - 127};
         } else {
-            const St x = slow_summary<IO>(sk + col + j, sv + col + j, kBwdC, n, (double)cc.w[j] * kLog2eD);
+            const St x = exact_summary<IO>(sk + col + j, sv + col + j, n, (double)cc.w[j] * kLog2eD);
             sum[j] = sum_of(x.a, x.b, x.p);
         }
     }
@@ -852,8 +917,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
                 const int64_t i = (int64_t)round * BC + jch;
                 carry = {p.ck_a[i], p.ck_b[i], p.ck_p[i]};
             } else if (p.state_in) {
-                carry = sum_of(p.state_in[jch], p.state_in[BC + jch],
-                               (double)p.state_in[2 * BC + jch] * kLog2eD);
+                carry = sum_of(p.state_in[jch], p.state_in[BC + jch], key2(p.state_in[2 * BC + jch]));
             }
         }
         cp_async_wait<1>();
@@ -979,10 +1043,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
                     if (rank > 0) wait(2 + ((turn - 1) & 1), ((turn - 1) >> 1) & 1);
                     s = after.get(((turn - 1) & 1) * kBwdC + jc);
                 } else if (jok && p.gstate_out) {
-                    const Sum x = sum_of(p.gstate_out[jch], p.gstate_out[BC + jch],
-                                         -(double)p.state_out[2 * BC + jch] * kLog2eD);
-                    const Decay d = decay_of(Rate{-rate.hi, -rate.lo}, rounds * round_steps - T);
-                    s = scaled(x.a * d.f, x.b * d.f, x.p + d.i);
+                    const Sum x = decayed(sum_of(p.gstate_out[jch], p.gstate_out[BC + jch],
+                                                 -key2(p.state_out[2 * BC + jch])),
+                                          decay_of(Rate{-rate.hi, -rate.lo}, rounds * round_steps - T));
+                    s = scaled(x.a, x.b, x.p);
                 }
             }
             if (rank < NC - 1) wait(1, parity);
@@ -1044,8 +1108,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
             if (!ok) gwj[j] = guj[j] = 0.f;
             if (t0 == 0 && ok && p.gstate_in) {
                 const int64_t sc = (int64_t)b * C + c + j;
-                const double f =
-                    exp2(fmin((double)R[j].p + (double)p.state_in[2 * BC + sc] * kLog2eD, 1000.0));
+                const double f = exp2(fmin(exponent_of(R[j].p) + key2(p.state_in[2 * BC + sc]), 1000.0));
                 const float ga = (float)(f * R[j].a), gb = (float)(f * R[j].b);
                 const float sa = p.state_in[sc], sb = p.state_in[BC + sc];
                 p.gstate_in[sc] = ga;
@@ -1151,7 +1214,7 @@ __global__ void __launch_bounds__(128) wkv4_backward_prefix_kernel(const BwdPara
     if (ch >= BC) return;
     const Decay d = decay_of(rate_of(p.w[ch % p.C]), (int)round_steps);
     Sum s = empty_sum();
-    if (p.state_in) s = sum_of(p.state_in[ch], p.state_in[BC + ch], (double)p.state_in[2 * BC + ch] * kLog2eD);
+    if (p.state_in) s = sum_of(p.state_in[ch], p.state_in[BC + ch], key2(p.state_in[2 * BC + ch]));
     constexpr int kAhead = 8;  // rounds loaded at once: the chain waits for memory once per group
     for (int r0 = 0; r0 < p.rounds; r0 += kAhead) {
         Sum x[kAhead];

@@ -186,3 +186,22 @@ def test_kernel_hash_leaves_out_the_units_the_bench_does_not_launch(tmp_path):
         if name not in bench._NOT_KERNEL_SOURCES:
             text = (copy / name).read_text()
             assert not any(f'#include "{other}"' in text for other in bench._NOT_KERNEL_SOURCES), name
+
+
+@pytest.mark.parametrize("state,gated", [(False, True), (True, False)])
+def test_oracle_of_any_range_is_the_oracle_for_usual_keys(state, gated):
+    x, gs = _case(2, 30, 3, 5, state, gated)
+    _, s_out = _loss(x, gs)
+    gso = np.stack([gs[0], gs[1], np.zeros_like(gs[0])])
+    args = (x["k"], x["v"], x["w"], x["u"], x["gy"], x["state_in"], x["r"], s_out, gso)
+    for a, b in zip(ob.wkv_backward(*args), ob.wkv_backward_any_range(*args)):
+        for name in a:
+            assert np.max(np.abs(a[name] - b[name])) <= 1e-12 * np.max(np.abs(a[name])), name
+    # a shift of all keys and of the state's max changes no gradient of a call that ends in no state
+    y = dict(x, k=x["k"] - 1e4)
+    if state:
+        y["state_in"] = x["state_in"] - np.array([0, 0, 1e4])[:, None, None]
+    a, _ = ob.wkv_backward(x["k"], x["v"], x["w"], x["u"], x["gy"], x["state_in"], x["r"])
+    b, _ = ob.wkv_backward_any_range(y["k"], y["v"], y["w"], y["u"], y["gy"], y["state_in"], y["r"])
+    for name in a:
+        assert np.max(np.abs(a[name] - b[name])) <= 1e-10 * np.max(np.abs(a[name])), name
