@@ -380,9 +380,16 @@ __device__ __forceinline__ St scaled_st(float P, float Q, double p) {
     return fabs(p) >= (double)kStillFrom ? St{P, Q, p} : St{x.a, x.b, p + (double)x.p};
 }
 
+// min(x, most), NaN where x is (fminf would return `most`).
+__device__ __forceinline__ float at_most(float x, float most) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(most));
+    return y;
+}
+
 // Gradients through the gate: g = s gout and, through the pointer, gr.
 __device__ __forceinline__ float gate_grad(float gout, float y, float r, float& gr) {
-    const float x = ex2(fminf(-r * kLog2e, 126.f));
+    const float x = ex2(at_most(-r * kLog2e, 126.f));
     const float s = rcp_approx(1.f + x);
     const float g = gout * s;
     gr = g * y * (x * s);
@@ -698,7 +705,7 @@ __device__ __forceinline__ void bwd_walk_up(const BwdChunk<IO>& ch, const BwdCon
                 if constexpr (kGate) {
                     const f2 x0 = mul2(load_f2<IO>(ch.r + i * kBwdC + ch.col), pk(-kLog2e, -kLog2e));
                     // (above 2^126 the gate is 0 to within its rounding, and x s stays finite)
-                    const f2 x = pk(ex2(fminf(lo(x0), 126.f)), ex2(fminf(hi(x0), 126.f)));
+                    const f2 x = pk(ex2(at_most(lo(x0), 126.f)), ex2(at_most(hi(x0), 126.f)));
                     const f2 sg = rcp2(add2(one, x));
                     g = mul2(g, sg);
                     const f2 grv = mul2(mul2(g, ny), mul2(x, sg)) ^ kSigns;
