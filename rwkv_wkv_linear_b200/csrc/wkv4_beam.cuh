@@ -169,14 +169,16 @@ struct BeamRow {
 
 // A thread's largest logit and its sum of e^{x - max}, as two sums of packed
 // pairs of 2^{x log2e - r} with r = max log2e rounded; nat() takes the rounding
-// back.  Where the product could overflow (|max| above 2^64) the difference is
-// taken before it is scaled.
+// back, to first order: below 2^11 it is at most 2^-13, so that what is left out
+// is under 2^-26.  From 2^11 on (masks, mostly) the difference is taken before
+// it is scaled: the rounding of r would be a factor of its own there, and past
+// 2^31 no float's.
 struct BeamSum {
     float max = -INFINITY;
     float r = 0.f;  // 0 before any finite logit: a NaN among those still ends up in the sum
     f2 sum = 0ull;
     bool far = false;
-    // max log2e - r, the rounding of r (at most 2^-25 of it)
+    // max log2e - r, the rounding of r (at most 2^-24 of it)
     __device__ __forceinline__ float rest() const {
         return far || max == -INFINITY ? 0.f : fmaf(max, kLog2e, -r);
     }
@@ -184,7 +186,7 @@ struct BeamSum {
         if (m > max) {
             const float f = ex2((max - m) * kLog2e), e = rest();  // max = -inf: 0
             max = m;
-            far = !(fabsf(m) < 0x1p64f);
+            far = !(fabsf(m) < 0x1p11f);
             r = m * kLog2e;
             const float c = f * fmaf(rest() - e, 0.6931472f, 1.f);  // from the old rounding to the new
             sum = mul2(sum, pk(c, c));
