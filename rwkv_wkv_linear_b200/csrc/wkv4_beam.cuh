@@ -307,6 +307,7 @@ __device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int 
                           const uint8_t* finished, BeamUnit* out, Ready ready) {
     typedef BeamVec<IO> V;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (finished && *finished) return;  // before the first load: its logits are not read
     const BeamRow<IO> row(p, len, v0);
     const int batches = (row.nvec + kBeamBatch * kBeamThreads - 1) / (kBeamBatch * kBeamThreads);
     uint4 x0[kBeamBatch], x1[kBeamBatch], x2[kBeamBatch];
@@ -315,7 +316,7 @@ __device__ void beam_unit(BeamShared& s, const IO* p, int len, uint32_t v0, int 
     const float lx = li >= 0 ? Io<IO>::to_f(p[li]) : -INFINITY;
     beam_load(row, 1, tid, x1);
     beam_load(row, 2, tid, x2);
-    if (!beam_alive(*score) || (finished && *finished)) return;
+    if (!beam_alive(*score)) return;
     BeamSum sum;
     float m = lx;
 #pragma unroll
