@@ -75,6 +75,11 @@ constexpr float kFastRange = 55.f;       // max k - min k (+ min(0, u)) within a
 constexpr float kFastStateLift = 44.f;   // carried state's max above the chunk's max k
 constexpr float kFastMaxU = 44.f;
 constexpr float kFastMaxW = 0.35f;
+// Largest |key| of a chunk held against one reference: the reference r = max k
+// log2(e) is rounded to fp32, and every e_i carries that rounding, half an ulp of
+// r, as a factor of its own.  Below 2^31 that is 2^64 at most, which the sums take
+// (their exponent has it back); a mask of -5e9 would make them infinite.
+constexpr float kFastMaxKey = 1.4e9f;
 
 
 
@@ -169,7 +174,8 @@ __device__ __forceinline__ float step_nat(St& s, float k, float v, float w, floa
 }
 
 __device__ __forceinline__ bool fast_ok(float kmax, float kmin, float u, float w) {
-    return (kmax - kmin <= kFastRange + fminf(0.f, u)) && (u <= kFastMaxU) && (w <= kFastMaxW);
+    return (kmax - kmin <= kFastRange + fminf(0.f, u)) && (u <= kFastMaxU) && (w <= kFastMaxW) &&
+           (fabsf(kmax) < kFastMaxKey);
 }
 
 // fp32 state buffers <-> kernel state.  On the way out the max is rounded to
