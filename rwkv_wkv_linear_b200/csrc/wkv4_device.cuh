@@ -184,9 +184,11 @@ __device__ __forceinline__ bool fast_ok(float kmax, float kmin, float u, float w
 // |d| < 2^-12 (a max below 4096 nats in magnitude, the usual case) e^d - 1
 // is d to within its last bit, and d is used as it is; beyond (a max of 10^5
 // nats after a long decay with nothing new has |d| up to 2^-5, where d alone
-// would be off by d^2 / 2) e^d - 1 comes from expm1f.
+// would be off by d^2 / 2) e^d - 1 comes from expm1f.  A max past 10^9 nats (a
+// state of masked steps alone) has |d| in the hundreds once it has decayed: held
+// to 80, a and b stay floats, and whatever usual key follows outweighs them.
 __device__ __forceinline__ float fold_factor(float d) {
-    return fabsf(d) < 0x1p-12f ? d : expm1f(d);
+    return fabsf(d) < 0x1p-12f ? d : expm1f(fminf(fmaxf(d, -80.f), 80.f));
 }
 __device__ __forceinline__ St load_state_log2(const float* __restrict__ s, int64_t BC, int64_t ch) {
     return {s[ch], s[BC + ch], (double)s[2 * BC + ch] * kLog2eD};
@@ -202,7 +204,9 @@ __device__ __forceinline__ void store_state_nat_d(float* __restrict__ s, int64_t
 }
 
 __device__ __forceinline__ void store_state_log2(float* __restrict__ s, int64_t BC, int64_t ch, St x) {
-    store_state_nat_d(s, BC, ch, x.a, x.b, x.p * kLn2D);
+    // (past 2^50 the products by log2(e) and ln 2 are off by nats themselves: the max as it is)
+    const double p = x.p * kLn2D;
+    store_state_nat_d(s, BC, ch, x.a, x.b, fabs(p) < 0x1p50 ? p : (double)(float)p);
 }
 
 // ---------------------------------------------------------------- I/O dtypes

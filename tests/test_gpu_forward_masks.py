@@ -1,5 +1,5 @@
 """The forward under finite masks of any size: whole chunks of keys like -1e10 or
--1e30 with nothing before them, in every kernel."""
+-1e30 with nothing before them, in every kernel, and the state they leave."""
 
 import pytest
 import torch
@@ -42,6 +42,7 @@ def test_masked_steps_weigh_nothing(cuda_device, T, masked, mask, kernel, dt):
     # (half a step of the type past the largest |v| before it, and the quotient's few roundings)
     most = v.float().abs().cummax(1).values[:, :masked] * (1 + 2.0 ** -8)
     assert torch.isfinite(head).all() and (head.abs() <= most).all()
+    assert torch.isfinite(s).all()
     if masked == T:
         return
     cut = [d(t[:, masked:].contiguous()) for t in (k, v)]
@@ -54,3 +55,20 @@ def test_masked_steps_weigh_nothing(cuda_device, T, masked, mask, kernel, dt):
     assert (y[:, masked:].float() - want.float()).abs().max().item() <= eps * vmax
     a, b = ((t[:2].double() * torch.exp(t[2].double())).cpu() for t in (s, sw))
     assert ((a - b).abs() <= 2.0 ** -24 * 512 * b[1].abs().clamp(min=0) * max(vmax, 1.0)).all()
+
+
+@pytest.mark.parametrize("mask", [-1e9, -1e10, -1e30])
+def test_a_masked_segment_carries_a_usable_state(cuda_device, mask):
+    """A segment of nothing but masks, with slow and fast decays, then a usual one on its state: the first leaves
+    no trace."""
+    B, T, C = 2, 1200, 64
+    k, v, w, u = _inputs(B, T, C, "f32", 3)
+    w[::2] *= 4.0
+    d = lambda t: t.to(cuda_device)
+    for kernel in KERNELS.values():
+        _, s = wkv4.forward(d(torch.full_like(k, mask)), d(v), d(w), d(u), variant=kernel)
+        assert torch.isfinite(s).all()
+        y, s2 = wkv4.forward(d(k), d(v), d(w), d(u), s, variant=kernel)
+        want, sw = wkv4.forward(d(k), d(v), d(w), d(u), variant=kernel)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(s2, sw)
