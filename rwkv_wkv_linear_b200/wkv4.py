@@ -139,6 +139,20 @@ def _one_device(**tensors) -> torch.device:
     return dev
 
 
+def _used_on(stream, dev: torch.device, *tensors):
+    """Tensors that a call on the caller's `stream` has allocated (None entries
+    skipped; nothing to do on the current stream): should the caller drop one at
+    once, its memory stays untouched until the stream has passed the call."""
+    if stream is None:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, device=dev)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _check_dev(name: str, t: Optional[torch.Tensor], dtype=None):
     if t is None:
         return
@@ -171,17 +185,21 @@ def forward(k: torch.Tensor, v: torch.Tensor, w: torch.Tensor, u: torch.Tensor,
         raise ValueError("w and u must be [C]")
     if state_in is not None and state_in.shape != (3, B, C):
         raise ValueError("state_in must be [3, B, C]")
+    own = []
     if y is None:
         y = torch.empty_like(k)
+        own.append(y)
     _check_dev("y", y, k.dtype)
     if state_out is None and want_state:
         state_out = torch.empty((3, B, C), dtype=torch.float32, device=k.device)
+        own.append(state_out)
     _check_dev("state_out", state_out, torch.float32)
     dev = _one_device(k=k, v=v, w=w, u=u, state_in=state_in, y=y, state_out=state_out)
     with torch.cuda.device(dev):
         rc = load().wkv4_forward_variant(B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v),
                                          _ptr(state_in), _ptr(y), _ptr(state_out),
                                          _stream(stream, dev), dt, int(variant))
+        _used_on(stream, dev, *own)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_forward")
     return y, state_out
@@ -210,17 +228,21 @@ def forward_gated(k: torch.Tensor, v: torch.Tensor, r: torch.Tensor, w: torch.Te
         raise ValueError("w and u must be [C]")
     if state_in is not None and state_in.shape != (3, B, C):
         raise ValueError("state_in must be [3, B, C]")
+    own = []
     if y is None:
         y = torch.empty_like(k)
+        own.append(y)
     _check_dev("y", y, k.dtype)
     if state_out is None and want_state:
         state_out = torch.empty((3, B, C), dtype=torch.float32, device=k.device)
+        own.append(state_out)
     _check_dev("state_out", state_out, torch.float32)
     dev = _one_device(k=k, v=v, r=r, w=w, u=u, state_in=state_in, y=y, state_out=state_out)
     with torch.cuda.device(dev):
         rc = load().wkv4_forward_gated_variant(B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r),
                                                _ptr(state_in), _ptr(y), _ptr(state_out),
                                                _stream(stream, dev), dt, int(variant))
+        _used_on(stream, dev, *own)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_forward_gated")
     return y, state_out
@@ -278,13 +300,15 @@ def forward_host(k: torch.Tensor, v: torch.Tensor, w: torch.Tensor, u: torch.Ten
     _check_host("state_out", state_out, torch.float32)
     dev = _one_device(w=w, u=u, workspace=workspace)
     need = host_workspace_bytes(B, T, C, k.dtype, r is not None, chunk_steps)
-    if workspace is None:
+    own = workspace is None
+    if own:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     _check_dev("workspace", workspace)
     with torch.cuda.device(dev):
         rc = load().wkv4_forward_host(B, T, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r),
                                       _ptr(state_in), _ptr(y), _ptr(state_out), _ptr(workspace),
                                       workspace.numel(), int(chunk_steps), _stream(stream, dev), dt)
+        _used_on(stream, dev, workspace if own else None)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_forward_host")
     return y, state_out
@@ -315,13 +339,15 @@ def decode_step(k: torch.Tensor, v: torch.Tensor, w: torch.Tensor, u: torch.Tens
     _check_dev("state", state, torch.float32)
     if state.shape != (3, B, C):
         raise ValueError("state must be [3, B, C]")
-    if y is None:
+    own = y is None
+    if own:
         y = torch.empty_like(k)
     _check_dev("y", y, k.dtype)
     dev = _one_device(k=k, v=v, w=w, u=u, state=state, y=y)
     with torch.cuda.device(dev):
         rc = load().wkv4_decode_step(B, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(state),
                                      _ptr(y), _stream(stream, dev), dt)
+        _used_on(stream, dev, y if own else None)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_decode_step")
     return y
@@ -345,13 +371,15 @@ def decode_step_gated(k: torch.Tensor, v: torch.Tensor, r: torch.Tensor, w: torc
     _check_dev("state", state, torch.float32)
     if state.shape != (3, B, C):
         raise ValueError("state must be [3, B, C]")
-    if y is None:
+    own = y is None
+    if own:
         y = torch.empty_like(k)
     _check_dev("y", y, k.dtype)
     dev = _one_device(k=k, v=v, r=r, w=w, u=u, state=state, y=y)
     with torch.cuda.device(dev):
         rc = load().wkv4_decode_step_gated(B, C, _ptr(w), _ptr(u), _ptr(k), _ptr(v), _ptr(r),
                                            _ptr(state), _ptr(y), _stream(stream, dev), dt)
+        _used_on(stream, dev, y if own else None)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_decode_step_gated")
     return y
@@ -379,7 +407,8 @@ def decode_step_slots(k: torch.Tensor, v: torch.Tensor, w: torch.Tensor, u: torc
         raise ValueError("state_pool must be [3, S, C]")
     if slot_ids.shape != (B,):
         raise ValueError("slot_ids must be [B]")
-    if y is None:
+    own = y is None
+    if own:
         y = torch.empty_like(k)
     _check_dev("y", y, k.dtype)
     dev = _one_device(k=k, v=v, w=w, u=u, state_pool=state_pool, slot_ids=slot_ids, y=y)
@@ -387,6 +416,7 @@ def decode_step_slots(k: torch.Tensor, v: torch.Tensor, w: torch.Tensor, u: torc
         rc = load().wkv4_decode_step_slots(B, C, state_pool.shape[1], _ptr(w), _ptr(u), _ptr(k),
                                            _ptr(v), _ptr(state_pool), _ptr(slot_ids), _ptr(y),
                                            _stream(stream, dev), dt)
+        _used_on(stream, dev, y if own else None)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_decode_step_slots")
     return y
@@ -419,6 +449,7 @@ def token_shift(x: torch.Tensor, mix_k: torch.Tensor, mix_v: torch.Tensor,
         rc = load().wkv4_token_shift(B, T, C, _ptr(x), _ptr(x_prev), _ptr(mix_k), _ptr(mix_v),
                                      _ptr(mix_r), _ptr(xk), _ptr(xv), _ptr(xr), _ptr(x_last),
                                      _stream(stream, dev), dt)
+        _used_on(stream, dev, xk, xv, xr)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_token_shift")
     return xk, xv, xr
@@ -436,13 +467,15 @@ def state_combine(x: Optional[torch.Tensor], y: torch.Tensor, n_steps: int, w: t
         _check_dev(name, t, torch.float32)
     if w.shape != (C,):
         raise ValueError("w must be [C]")
-    if out is None:
+    own = out is None
+    if own:
         out = torch.empty_like(y)
     _check_dev("out", out, torch.float32)
     dev = _one_device(x=x, y=y, w=w, out=out)
     with torch.cuda.device(dev):
         rc = load().wkv4_state_combine(B, C, _ptr(w), int(n_steps), _ptr(x), _ptr(y), _ptr(out),
                                        _stream(stream, dev))
+        _used_on(stream, dev, out if own else None)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_state_combine")
     return out
@@ -527,11 +560,7 @@ def _workspace(given: Optional[torch.Tensor], need: int, dev: torch.device, stre
     if need == 0:
         return None
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-            stream = torch.cuda.ExternalStream(raw, device=dev)
-        ws.record_stream(stream)
+    _used_on(stream, dev, ws)
     return ws
 
 
@@ -571,6 +600,7 @@ def backward(k: torch.Tensor, v: torch.Tensor, w: torch.Tensor, u: torch.Tensor,
                                gk.data_ptr(), gv.data_ptr(), _adr(gr), gw.data_ptr(), gu.data_ptr(),
                                _adr(gs), _adr(ws), 0 if ws is None else ws.numel(),
                                _raw_stream(stream, dev), dt)
+        _used_on(stream, dev, gk, gv, gr, gw, gu, gs)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_backward")
     return Grads(gk, gv, gr, gw, gu, gs)
@@ -618,6 +648,7 @@ def token_shift_backward(x: torch.Tensor, mix_k: torch.Tensor, mix_v: torch.Tens
                                            _adr(gxr), _adr(gx_last), gx.data_ptr(), _adr(gp),
                                            gk.data_ptr(), gv.data_ptr(), _adr(gr), _adr(ws),
                                            0 if ws is None else ws.numel(), _raw_stream(stream, dev), dt)
+        _used_on(stream, dev, gx, gp, gk, gv, gr)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_token_shift_backward")
     return ShiftGrads(gx, gk, gv, gr, gp)
@@ -662,6 +693,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n: Optional[int] = N
         rc = lib.wkv4_beam_select(G, K, V, ld, n, logits.data_ptr(), scores.data_ptr(), _adr(finished),
                                   int(end_id), out.data_ptr(), parents.data_ptr(), tokens.data_ptr(),
                                   _raw_stream(stream, dev), dt)
+        _used_on(stream, dev, out, parents, tokens)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_beam_select")
     return out, parents, tokens
@@ -683,7 +715,8 @@ def state_reorder(pool: torch.Tensor, slot_ids: torch.Tensor, parents: torch.Ten
     if slot_ids.dim() != 2:
         raise ValueError("slot_ids must be [G, K]")
     dev = _cuda("pool", pool)
-    if new_slot_ids is None:
+    own = new_slot_ids is None
+    if own:
         new_slot_ids = torch.empty_like(slot_ids)
     _require(dev, pool.dtype, pool=pool)
     _require(dev, torch.int32, slot_ids=slot_ids, parents=parents, new_slot_ids=new_slot_ids)
@@ -694,6 +727,7 @@ def state_reorder(pool: torch.Tensor, slot_ids: torch.Tensor, parents: torch.Ten
         rc = lib.wkv4_state_reorder(P, S, C, G, K, pool.data_ptr(), slot_ids.data_ptr(),
                                     parents.data_ptr(), new_slot_ids.data_ptr(),
                                     _raw_stream(stream, dev), dt)
+        _used_on(stream, dev, new_slot_ids if own else None)
     if rc != 0:
         raise Wkv4Error(rc, "wkv4_state_reorder")
     return new_slot_ids
