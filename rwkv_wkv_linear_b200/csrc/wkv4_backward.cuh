@@ -777,6 +777,14 @@ __device__ __forceinline__ void bwd_walk_down(const BwdChunk<IO>& ch, const BwdC
     }
 }
 
+// gk of a step with nothing before it: y is v, so the step's own share of it (and
+// of gu) is 0, not what the approximate reciprocal leaves of v - y, which may be
+// all there is.  From (P, Q) behind it, against the reference 2^R.
+template <typename IO>
+__device__ __noinline__ IO first_step_gk(IO k, IO v, float R, float P, float Q) {
+    return Io<IO>::from_f(ex2(fmaf(Io<IO>::to_f(k), kLog2e, -R)) * fmaf(P, Io<IO>::to_f(v), Q));
+}
+
 // kOne: T fits one round.  The loop over rounds and what lives across it fall
 // away, and with them the spills at 168 registers (B=4, T=1024, C=5120, bf16,
 // gated: 95.7 us against 105.6; B=8, T=1024, C=768, fp16: 34.4 against 37.3).
@@ -1098,6 +1106,16 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
         } else {
             bwd_walk_down<IO, L, false>(ch, cc, nref, Pw, Qw, gk, gv, C, p.vec_store, ok0 && fastR[0],
                                      ok1 && fastR[1]);
+            if (n == 1) {
+                if (ok0 && fastR[0] && S[0].b == 0.f) {
+                    gk[0] = first_step_gk(ch.k[col], ch.v[col], ref.R[0], p0[0], q0f[0]);
+                    up.gu = pk(0.f, hi(up.gu));
+                }
+                if (ok1 && fastR[1] && S[1].b == 0.f) {
+                    gk[1] = first_step_gk(ch.k[col + 1], ch.v[col + 1], ref.R[1], p0[1], q0f[1]);
+                    up.gu = pk(lo(up.gu), 0.f);
+                }
+            }
         }
         float gwj[2] = {lo(gw), hi(gw)}, guj[2] = {lo(up.gu), hi(up.gu)};
         const float Pe[2] = {lo(Pw), hi(Pw)}, Qe[2] = {lo(Qw), hi(Qw)};
