@@ -64,13 +64,15 @@
 // gw and gu are summed in fp32: a thread's steps, then the warps, then
 // (wkv4_column_sum_kernel) the CTAs, in a fixed order.
 //
-// What bounds it.  B=4, T=1024, C=5120, bf16, gated: 95.8 us for 294 MB (3.1 TB/s)
-// and 159 warp instructions a step of 64 channels at 2.2 a clock and SM: issue,
+// What bounds it.  B=4, T=1024, C=5120, bf16, gated: 95.3 us for 294 MB (3.1 TB/s)
+// and 161 warp instructions a step of 64 channels at 2.2 a clock and SM: issue,
 // with 12 warps an SM (by shared memory and registers alike) to cover the
 // instructions' latencies, not HBM.  A fourth CTA an SM costs more in spills
 // than it hides; al, y in tensor memory instead of shared memory are what makes
-// three fit.  B=1, T=16384, C=2048, fp32, with k, v read twice: 227 us for 940 MB
-// (4.1 TB/s).  Short calls are a chain of latencies: B=1, T=48, C=768 5.6 us.
+// three fit.  B=1, T=16384, C=2048, fp32, with k, v read twice: 229 us for 940 MB
+// (4.1 TB/s).  Short calls are a chain of latencies: B=1, T=48, C=768 5.9 us.
+// Masked steps are not fast: with the last quarter of the 14B width's keys at
+// -inf, or its first at -1e9, the exact path makes it 822 or 702 us.
 #pragma once
 
 #include <cooperative_groups.h>

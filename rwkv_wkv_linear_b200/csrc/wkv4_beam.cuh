@@ -20,19 +20,21 @@
 //     the pass the threads' maxima are those of the whole unit: the looser bound
 //     taken from them once more leaves some two n of the pieces' elements, which
 //     are ranked by counting;
-//   * where either list overflows (many equal logits) the n largest are found
-//     one by one, each a pass over the unit.
+//   * where either list overflows (many equal logits, or a first batch well below
+//     the rest: a script-ordered vocabulary, its first tokens ruled out) the n
+//     largest are found one by one, each a pass over the unit (the batch below
+//     takes 340 us then).
 // Logits of one row order like their scores, so only n a unit matter; the
 // first CTA of the cluster receives the units' lists and sums through cluster
 // shared memory and computes the scores in fp64.  The lists being in order, a
 // candidate's rank is its place in its own plus what bisection finds before it
 // in each other.
 //
-// What bounds it.  48 requests of 8 beams over 50277 bf16 logits, n = 16: 21.0 us
+// What bounds it.  48 requests of 8 beams over 50277 bf16 logits, n = 16: 20.9 us
 // for 38.6 MB (1.8 TB/s); 2 or 3 rows an SM, whose pass ends after about 12 us,
 // the rest being the latencies of ranking, cluster barrier and merge.  (With an
 // eighth of the exponentials on the FMA units it takes 21.1 us, with the looser
-// first bound alone 22.3.)  One request of 4 beams, fp32: 8.4 us, the chain of
+// first bound alone 22.3.)  One request of 4 beams, fp32: 8.6 us, the chain of
 // latencies alone: three batches of loads are in flight a thread.
 #pragma once
 
