@@ -1109,11 +1109,11 @@ __global__ void __launch_bounds__(32 * kBwdWarps, BwdLayout<IO, L, kGate>::kCtas
             bwd_walk_down<IO, L, false>(ch, cc, nref, Pw, Qw, gk, gv, C, p.vec_store, ok0 && fastR[0],
                                      ok1 && fastR[1]);
             if (n == 1) {
-                if (ok0 && fastR[0] && S[0].b == 0.f) {
+                if (ok0 && fastR[0] && S[0].a == 0.f && S[0].b == 0.f) {
                     gk[0] = first_step_gk(ch.k[col], ch.v[col], ref.R[0], p0[0], q0f[0]);
                     up.gu = pk(0.f, hi(up.gu));
                 }
-                if (ok1 && fastR[1] && S[1].b == 0.f) {
+                if (ok1 && fastR[1] && S[1].a == 0.f && S[1].b == 0.f) {
                     gk[1] = first_step_gk(ch.k[col + 1], ch.v[col + 1], ref.R[1], p0[1], q0f[1]);
                     up.gu = pk(lo(up.gu), 0.f);
                 }

@@ -46,3 +46,12 @@ def test_zero_state_given(cuda_device):
     g = wkv4.backward(d["k"], d["v"], d["w"], d["u"], d["gy"], s)
     torch.cuda.synchronize()
     assert not g.gk.any() and not g.gu.any() and not g.gstate_in.any()
+
+
+def test_a_state_with_a_numerator_alone(cuda_device):
+    """A state whose denominator is zero is not an empty one: y is not v."""
+    x = _inputs(2, 1, 40, "f32", seed=4, gated=False, state=True)
+    x["state_in"][1] = 0
+    g, s = _run(x, cuda_device)
+    _check(x, g, s, "f32", "numerator alone")
+    assert g.gk.any()
